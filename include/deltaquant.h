@@ -545,6 +545,82 @@ int dq_linear_forward_host_ex(const void* X_host, int T, int H, int W, int t, in
 int dq_linear_forward_noalloc(const void* X, int T, int H, int W, int t, int h, int w, int Ci, int Co, int rank,
                               const void* packed_W, const void* L1_mma, const void* L2_slab, void* Y, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Few rows: a normalisation and the product beside the cube layers           */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Row formats of the two entry points below.  A quantised row holds E4M3 codes
+ * and fp32 scales, with the granularities of the kernel tokens
+ * (DQ_KERNEL_SCALE_*): value = code * scale.
+ *   DQ_ROWS_BF16          BF16 values, no scales
+ *   DQ_ROWS_E4M3          E4M3 codes, one scale per row: scales[row]
+ *   DQ_ROWS_E4M3_GROUP64  E4M3 codes, one scale per 64 channels:
+ *                         scales[row * ceil(C / 64) + channel / 64] (the last
+ *                         group of a row holds the channels that are left)
+ */
+#define DQ_ROWS_BF16 0
+#define DQ_ROWS_E4M3 1
+#define DQ_ROWS_E4M3_GROUP64 2
+
+/*
+ * Root-mean-square norm of rows with the residual's addition, BF16 or 8 bits out:
+ *   h   = x + residual                 (fp32; h = x where residual is NULL)
+ *   sum = BF16(h)                      (written where sum_out is not NULL)
+ *   y   = h / sqrt(mean_c h^2 + eps) * gamma      (fp32; gamma NULL: 1)
+ *   Y   = BF16(y), or E4M3(y / s) with s = max |y| / 448 over the row or over
+ *         each 64 channels (codes 0 where s is 0), s written to y_scales.
+ * The norm is taken of the unrounded fp32 h.
+ *   X, residual, sum_out   device BF16, rows x C, row strides in elements
+ *   gamma                  device BF16, C values, or NULL
+ *   Y                      device, BF16 or E4M3 codes by y_format (DQ_ROWS_*)
+ *   y_scales               device fp32, as the format says (NULL for BF16)
+ *   eps                    >= 0 and finite
+ * Strides are in elements, at least C; 0 stands for C (and, with a NULL
+ * pointer, is ignored).  rows >= 0 (0: nothing is done), 1 <= C <= 32768, any
+ * width, stride and element-aligned pointer; rows whose pointers and strides
+ * are 16-byte aligned (8 bytes for codes) and whose C is a multiple of 8 take
+ * wide loads.  sum_out may be X or residual itself with the same stride, and Y
+ * may be X with the same stride (BF16); no other two buffers may overlap.
+ * Only the C values of each row are written.  A row with a NaN or an infinity
+ * gives what the formula gives (NaN, and NaN scales).  One launch, no
+ * workspace.  Any alignment of the elements' size is accepted (scales: 4
+ * bytes), DQ_ERR_ALIGNMENT otherwise.
+ */
+int dq_rmsnorm_forward(const void* X, long long x_stride, const void* residual, long long residual_stride,
+                       const void* gamma, long long rows, int C, float eps, void* sum_out, long long sum_stride,
+                       int y_format, void* Y, long long y_stride, float* y_scales, void* stream);
+
+/*
+ * The product of few rows with a packed weight (conditioning vectors, one token
+ * a frame, a prompt's tokens: rows that form no lattice):
+ *   Y[m] = act( S_W sum_c xv[m][c] (q s_b)[o][c] + (xv[m] L1) L2  [+ b] )
+ * xv is the row itself, not quantised further: BF16 values, or the values that
+ * E4M3 codes and their scales stand for (x_format, DQ_ROWS_*).  act is the
+ * identity or GELU (epilogue, DQ_EPILOGUE_*).  Sums are fp32, one rounding to
+ * BF16 at the end.
+ *   X        device, rows x Ci, BF16 (x_stride a multiple of 8) or E4M3 codes (a
+ *            multiple of 16), 16-byte aligned
+ *   x_scales device fp32, contiguous, as the format says (4-byte aligned); NULL
+ *            for BF16
+ *   packed_W, L1_mma, L2_slab   device, as dq_pack_weight makes them (with or
+ *            without DQ_PACK_C2: only codes, scales and bias are read)
+ *   Y        device BF16, rows x Co (2-byte aligned)
+ * Strides are in elements, at least the row's width; 0 stands for that width.
+ * rows in [0, 65535] (0: nothing is done); Ci, Co and rank as everywhere.
+ * workspace: at least dq_rows_workspace_bytes(rows, ...) bytes of device
+ * memory; a larger row count's workspace serves smaller ones too.  Calls that
+ * may overlap need workspaces of their own (two captured graphs too).  Every
+ * call sets the status word (dq_read_device_status) anew: a packed weight that
+ * does not match is DQ_ERR_BAD_PACKED_WEIGHT, and Y is then not written.  A row
+ * of X with a NaN or an infinity gives a row of NaN.  Only the Co values of each
+ * row of Y are written; Y must not overlap X.
+ */
+int dq_rows_workspace_bytes(int rows, int Ci, int Co, int rank, size_t* bytes);
+int dq_rows_forward(const void* X, int x_format, long long x_stride, const float* x_scales, int rows, int Ci, int Co,
+                    int rank, const void* packed_W, const void* L1_mma, const void* L2_slab, int epilogue, void* Y,
+                    long long y_stride, void* workspace, size_t workspace_bytes, void* stream);
+
 /* The workspace argument of dq_read_device_status that names the fixed array
  * of dq_linear_forward_noalloc. */
 #define DQ_NOALLOC_WORKSPACE ((const void*)1)

@@ -43,6 +43,7 @@ DQ_DELTA_SCALE_AMAX, DQ_DELTA_SCALE_POW2 = 0, 1
 DQ_HOST_OVERLAP_PREVIOUS = 1
 DQ_EPILOGUE_NONE, DQ_EPILOGUE_GELU = 0, 1
 DQ_FFN_SEPARATE_STATISTICS = 1
+DQ_ROWS_BF16, DQ_ROWS_E4M3, DQ_ROWS_E4M3_GROUP64 = 0, 1, 2
 
 
 class dq_packed_layout(ctypes.Structure):
@@ -105,6 +106,9 @@ _SIGS = {
     "dq_ffn_forward_opts": ([_P, _I, _I, _I, _P, _P] + [_I] * 5 +
                             [ctypes.POINTER(dq_forward_options), ctypes.POINTER(dq_forward_options)] + [_P] * 8 +
                             [_P, _SZ, _P, _SZ, _I, _P, _P], _I),
+    "dq_rmsnorm_forward": ([_P, _LL, _P, _LL, _P, _LL, _I, ctypes.c_float, _P, _LL, _I, _P, _LL, _P, _P], _I),
+    "dq_rows_workspace_bytes": ([_I] * 4 + [ctypes.POINTER(_SZ)], _I),
+    "dq_rows_forward": ([_P, _I, _LL, _P] + [_I] * 4 + [_P] * 3 + [_I, _P, _LL, _P, _SZ, _P], _I),
     "dq_selftest_bounded_wait": ([_I, _P, ctypes.POINTER(_I)], _I),
     "dq_selftest_convert": ([_P, _LL, _P, _P, _P, _P], _I),
     "dq_selftest_gelu": ([_P, _LL, _P, _P], _I),
@@ -430,6 +434,53 @@ def dq_linear_forward_noalloc(X, T, H, W, t, h, w, Ci, Co, rank, packed_W, L1_mm
     _check("dq_linear_forward_noalloc",
            _lib.dq_linear_forward_noalloc(_ptr(X), T, H, W, t, h, w, Ci, Co, rank, _ptr(packed_W), _ptr(L1_mma),
                                           _ptr(L2_slab), _ptr(Y), _stream(stream)))
+
+
+# ------------------------------------------------------------------ few rows (device)
+
+def _same_device(fn: str, *tensors) -> None:
+    """The library launches on the current CUDA device: refuse torch tensors that live elsewhere."""
+    dev = None
+    for x in tensors:
+        if x is None or isinstance(x, int) or not hasattr(x, "get_device"):
+            continue
+        d = x.get_device()
+        if dev is None:
+            import torch
+            dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
+        if d != dev:
+            where = "in host memory" if d < 0 else f"on device {d}"
+            raise ValueError(f"{fn}: a tensor is {where}, the current CUDA device is {dev}")
+
+
+def dq_rmsnorm_forward(X, rows: int, C: int, Y, x_stride: int = 0, residual=None, residual_stride: int = 0,
+                       sum_out=None, sum_stride: int = 0, gamma=None, eps: float = 1e-6, y_format: int = DQ_ROWS_BF16,
+                       y_stride: int = 0, y_scales=None, stream=None) -> None:
+    """Y = RMS norm of X + residual, in BF16 or E4M3 with scales; sum_out = BF16(X + residual).
+    Strides in elements, 0 for contiguous rows (include/deltaquant.h)."""
+    _same_device("dq_rmsnorm_forward", X, residual, sum_out, gamma, Y, y_scales)
+    rc = _lib.dq_rmsnorm_forward(_ptr(X), x_stride, _ptr(residual), residual_stride, _ptr(gamma), rows, C, eps,
+                                 _ptr(sum_out), sum_stride, y_format, _ptr(Y), y_stride, _ptr(y_scales),
+                                 _stream(stream))
+    _check("dq_rmsnorm_forward", rc)
+
+
+def dq_rows_workspace_bytes(rows: int, Ci: int, Co: int, rank: int) -> int:
+    b = _SZ()
+    _check("dq_rows_workspace_bytes", _lib.dq_rows_workspace_bytes(rows, Ci, Co, rank, ctypes.byref(b)))
+    return b.value
+
+
+def dq_rows_forward(X, rows: int, Ci: int, Co: int, rank: int, packed_W, L1_mma, L2_slab, Y, workspace,
+                    workspace_bytes: int, x_stride: int = 0, x_format: int = DQ_ROWS_BF16, x_scales=None,
+                    epilogue: int = DQ_EPILOGUE_NONE, y_stride: int = 0, stream=None) -> None:
+    """Y = the packed layer applied to few rows that are not quantised further: BF16, or E4M3 codes
+    with scales (x_format, x_scales).  Strides in elements, 0 for contiguous rows (include/deltaquant.h)."""
+    _same_device("dq_rows_forward", X, x_scales, packed_W, L1_mma, L2_slab, Y, workspace)
+    rc = _lib.dq_rows_forward(_ptr(X), x_format, x_stride, _ptr(x_scales), rows, Ci, Co, rank, _ptr(packed_W),
+                              _ptr(L1_mma), _ptr(L2_slab), epilogue, _ptr(Y), y_stride, _ptr(workspace),
+                              workspace_bytes, _stream(stream))
+    _check("dq_rows_forward", rc)
 
 
 def dq_read_device_status(workspace=None, stream=None, clear: bool = False) -> int:

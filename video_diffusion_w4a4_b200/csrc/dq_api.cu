@@ -137,6 +137,12 @@ int check_shape(int T, int H, int W, int t, int h, int w, int Ci, int Co, int ra
     return DQ_OK;
 }
 
+int check_rows_shape(int rows, int Ci, int Co, int rank) {
+    if (rows < 0) return DQ_ERR_INVALID_ARG;
+    if (rows > 65535) return DQ_ERR_UNSUPPORTED_SHAPE;
+    return check_shape(1, 1, 1, 1, 1, 1, Ci, Co, rank);
+}
+
 int check_options(const dq_forward_options& o) {
     if (o.kernel_group != DQ_KERNEL_SCALE_PER_TOKEN && o.kernel_group != DQ_KERNEL_SCALE_GROUP64)
         return DQ_ERR_INVALID_ARG;
@@ -798,6 +804,101 @@ int dq_linear_forward_host_ex(const void* X_host, int T, int H, int W, int t, in
     if ((e = cudaEventRecord(done, aux->out)) != cudaSuccess || (e = cudaStreamWaitEvent(st, done, 0)) != cudaSuccess)
         return cuda_fail(e, "stream order");
     return DQ_OK;
+}
+
+int dq_rmsnorm_forward(const void* X, long long x_stride, const void* residual, long long residual_stride,
+                       const void* gamma, long long rows, int C, float eps, void* sum_out, long long sum_stride,
+                       int y_format, void* Y, long long y_stride, float* y_scales, void* stream) {
+    if (rows < 0 || C < 1 || !(eps >= 0.f) || eps > 3.0e38f) return DQ_ERR_INVALID_ARG;
+    if (y_format != DQ_ROWS_BF16 && y_format != DQ_ROWS_E4M3 && y_format != DQ_ROWS_E4M3_GROUP64) return DQ_ERR_INVALID_ARG;
+    if (rows >= (1ll << 31) || C > 32768) return DQ_ERR_UNSUPPORTED_SHAPE;
+    const bool codes = y_format != DQ_ROWS_BF16;
+    if (codes != (y_scales != nullptr)) return DQ_ERR_INVALID_ARG;
+    if (x_stride == 0) x_stride = C;
+    if (residual_stride == 0) residual_stride = C;
+    if (sum_stride == 0) sum_stride = C;
+    if (y_stride == 0) y_stride = C;
+    if (x_stride < C || (residual && residual_stride < C) || (sum_out && sum_stride < C) || y_stride < C)
+        return DQ_ERR_INVALID_ARG;
+    if (rows == 0) return DQ_OK;
+    if (!X || !Y) return DQ_ERR_INVALID_ARG;
+    if (((uintptr_t)X | (uintptr_t)residual | (uintptr_t)gamma | (uintptr_t)sum_out | (codes ? 0 : (uintptr_t)Y)) & 1)
+        return DQ_ERR_ALIGNMENT;
+    if ((uintptr_t)y_scales & 3) return DQ_ERR_ALIGNMENT;
+    dq::NormParams p;
+    memset(&p, 0, sizeof(p));
+    p.x = (const uint16_t*)X;
+    p.residual = (const uint16_t*)residual;
+    p.gamma = (const uint16_t*)gamma;
+    p.sum = (uint16_t*)sum_out;
+    p.y = Y;
+    p.scales = y_scales;
+    p.x_stride = x_stride;
+    p.r_stride = residual_stride;
+    p.s_stride = sum_stride;
+    p.y_stride = y_stride;
+    p.rows = rows;
+    p.C = C;
+    p.group = y_format == DQ_ROWS_E4M3_GROUP64 ? 64 : 0;
+    p.eps = eps;
+    cudaError_t e = dq::launch_rmsnorm(p, (cudaStream_t)stream);
+    return e == cudaSuccess ? DQ_OK : cuda_fail(e, "k_rmsnorm");
+}
+
+int dq_rows_workspace_bytes(int rows, int Ci, int Co, int rank, size_t* bytes) {
+    if (!bytes) return DQ_ERR_INVALID_ARG;
+    const int rc = check_rows_shape(rows, Ci, Co, rank);
+    if (rc) return rc;
+    *bytes = dq::rows_layout(rows, rank).total;
+    return DQ_OK;
+}
+
+int dq_rows_forward(const void* X, int x_format, long long x_stride, const float* x_scales, int rows, int Ci, int Co,
+                    int rank, const void* packed_W, const void* L1_mma, const void* L2_slab, int epilogue, void* Y,
+                    long long y_stride, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_rows_shape(rows, Ci, Co, rank);
+    if (rc) return rc;
+    if (x_format != DQ_ROWS_BF16 && x_format != DQ_ROWS_E4M3 && x_format != DQ_ROWS_E4M3_GROUP64) return DQ_ERR_INVALID_ARG;
+    if (epilogue != DQ_EPILOGUE_NONE && epilogue != DQ_EPILOGUE_GELU) return DQ_ERR_INVALID_ARG;
+    const bool codes = x_format != DQ_ROWS_BF16;
+    if (codes != (x_scales != nullptr)) return DQ_ERR_INVALID_ARG;
+    if (x_stride == 0) x_stride = Ci;
+    if (y_stride == 0) y_stride = Co;
+    if (x_stride < Ci || y_stride < Co) return DQ_ERR_INVALID_ARG;
+    if (rows == 0) return DQ_OK;
+    if (!X || !packed_W || !L1_mma || !L2_slab || !Y || !workspace) return DQ_ERR_INVALID_ARG;
+    if (((uintptr_t)X & 15) || x_stride % (codes ? 16 : 8) || ((uintptr_t)x_scales & 3) || ((uintptr_t)Y & 1))
+        return DQ_ERR_ALIGNMENT;
+    if (!aligned(packed_W) || !aligned(L1_mma) || !aligned(L2_slab) || !aligned(workspace)) return DQ_ERR_ALIGNMENT;
+    const dq::RowsLayout wl = dq::rows_layout(rows, rank);
+    if (workspace_bytes < wl.total) return DQ_ERR_WORKSPACE_TOO_SMALL;
+    const dq::PackedLayout pl = dq::packed_layout(Co, Ci, rank);
+    uint8_t* ws = (uint8_t*)workspace;
+    dq::RowsParams p;
+    memset(&p, 0, sizeof(p));
+    p.x = X;
+    p.x_scales = x_scales;
+    p.x_stride = x_stride;
+    p.y_stride = y_stride;
+    p.x_format = x_format;
+    p.rows = rows;
+    p.Ci = Ci;
+    p.Co = Co;
+    p.rank = rank;
+    p.slab = pl.slab;
+    p.gelu = epilogue == DQ_EPILOGUE_GELU;
+    p.packed_w = (const uint8_t*)packed_W;
+    p.off_codes = pl.off_codes;
+    p.off_scales = pl.off_scales;
+    p.off_bias = pl.off_bias;
+    p.l1 = (const uint16_t*)L1_mma;
+    p.l2 = (const uint16_t*)L2_slab;
+    p.y = (uint16_t*)Y;
+    p.status = (int*)(ws + wl.off_status);
+    p.u = (float*)(ws + wl.off_u);
+    p.budget_ns = kWaitBudgetNs;
+    cudaError_t e = dq::launch_rows(p, (cudaStream_t)stream);
+    return e == cudaSuccess ? DQ_OK : cuda_fail(e, "few-row product");
 }
 
 int dq_read_device_status(const void* workspace, void* stream, int* status, int clear) {

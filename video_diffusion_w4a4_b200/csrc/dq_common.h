@@ -228,4 +228,18 @@ DQ_HD WsLayout ws_layout(const Geom& g, int Ci, int Co, int rank, int kgroup = 0
     return L;
 }
 
+// Workspace of dq_rows_forward: the status word, then U = X L1 (rows x rank fp32).
+struct RowsLayout {
+    size_t total, off_status, off_u;
+};
+
+DQ_HD RowsLayout rows_layout(int rows, int rank) {
+    RowsLayout L;
+    size_t off = 0;
+    L.off_status = off;  off = align_up(off + 16, kAlign);
+    L.off_u = off;       off = align_up(off + (size_t)rows * rank * 4, kAlign);
+    L.total = off;
+    return L;
+}
+
 }  // namespace dq

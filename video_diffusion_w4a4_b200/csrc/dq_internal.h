@@ -104,6 +104,40 @@ cudaError_t launch_main_gemm_ffn(const CUtensorMap& tm_a, const CUtensorMap& tm_
                                  const CUtensorMap& tm_sb, const CUtensorMap& tm_fa, const CUtensorMap& tm_fb,
                                  const GemmParams& p, cudaStream_t st);
 
+// Root-mean-square norm of rows (dq_norm.cu); strides in elements
+struct NormParams {
+    const uint16_t* x;
+    const uint16_t* residual;   // null: h = x
+    const uint16_t* gamma;      // null: 1
+    uint16_t* sum;              // null: not written
+    void* y;                    // BF16, or E4M3 codes when scales is set
+    float* scales;
+    long long x_stride, r_stride, s_stride, y_stride, rows;
+    int C;
+    int group;                  // channels per scale; 0: one per row
+    float eps;
+};
+cudaError_t launch_rmsnorm(const NormParams& p, cudaStream_t st);
+
+// Product of few rows with a packed weight (dq_rows.cu)
+struct RowsParams {
+    const void* x;
+    const float* x_scales;
+    long long x_stride, y_stride;
+    int x_format;               // DQ_ROWS_*
+    int rows, Ci, Co, rank, slab;
+    int gelu;
+    const uint8_t* packed_w;
+    size_t off_codes, off_scales, off_bias;
+    const uint16_t* l1;         // rank x Ci
+    const uint16_t* l2;         // Co x slab
+    uint16_t* y;
+    int* status;
+    float* u;                   // rows x rank
+    uint64_t budget_ns;
+};
+cudaError_t launch_rows(const RowsParams& p, cudaStream_t st);
+
 // Device address of the no-allocation entry point's fixed workspace on the
 // current device (dq_noalloc.cu); a dq_status code.
 int noalloc_workspace(void** out);

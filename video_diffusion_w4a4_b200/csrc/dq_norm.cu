@@ -1,0 +1,246 @@
+// Root-mean-square norm of rows with the residual's addition (dq_rmsnorm_forward).
+//
+//   h = x + residual (fp32), sum = BF16(h),
+//   y = h / sqrt(mean h^2 + eps) * gamma, stored as BF16 or as E4M3 codes with
+//   s = max |y| / 448 per row or per 64 channels (the kernel tokens' rule).
+//
+// Bound by HBM: a row is read once into registers (pieces of eight channels, up
+// to kMaxItems a thread), its sum of squares and maxima are formed there, and
+// everything is written from there.  A row takes one CTA, or one warp when it
+// has at most 1024 channels, so that narrow rows need no block-wide step.
+// Eight neighbouring lanes hold 64 channels, so a group's maximum is three
+// shuffles.  Pointers, strides and widths that do not allow 16-byte pieces take
+// the same code with element accesses.
+#include <math.h>
+
+#include "dq_common.h"
+#include "dq_internal.h"
+#include "dq_ptx.cuh"
+
+namespace dq {
+
+namespace {
+
+constexpr int kMaxItems = 4;        // pieces of eight channels per thread
+constexpr int kWarpRows = 4;        // rows per CTA when a row takes one warp
+
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Reduction over the threads of a row: a warp, or the whole CTA (every thread gets the result; each
+// call uses its own 32 words of `sh`).
+template <bool kWarp, typename T, typename Op>
+__device__ __forceinline__ T row_reduce(T v, T* sh, Op op) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if (!kWarp) {
+        const int nw = (int)(blockDim.x >> 5), lane = threadIdx.x & 31;
+        if (lane == 0) sh[threadIdx.x >> 5] = v;
+        __syncthreads();
+        T r = sh[0];
+        for (int w = 1; w < nw; w++) r = op(r, sh[w]);
+        v = r;
+    }
+    return v;
+}
+
+// Eight channels from c0 on (those below C); BF16 bits, the low half of a word first.
+template <bool kWide>
+__device__ __forceinline__ void load8(const uint16_t* src, int c0, int C, uint32_t (&w)[4]) {
+    if (kWide) {
+        const uint4 v = *reinterpret_cast<const uint4*>(src + c0);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint32_t lo = c0 + 2 * i < C ? src[c0 + 2 * i] : 0, hi = c0 + 2 * i + 1 < C ? src[c0 + 2 * i + 1] : 0;
+            w[i] = lo | (hi << 16);
+        }
+    }
+}
+
+template <bool kWide>
+__device__ __forceinline__ void store8(uint16_t* dst, int c0, int C, const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) w[i] = bf16x2_rn(v[2 * i], v[2 * i + 1]);
+    if (kWide) {
+        *reinterpret_cast<uint4*>(dst + c0) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (c0 + i < C) dst[c0 + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+// E4M3 codes of y / s, correctly rounded quotients; 0 where s is 0.
+template <bool kWide>
+__device__ __forceinline__ void store_codes8(uint8_t* dst, int c0, int C, const float (&y)[8], float s) {
+    uint32_t w[2] = {0, 0};
+    if (s > 1e-30f && s < 1e30f) {
+        const float rs = __frcp_rn(s);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            w[i / 2] |= cvt_e4m3x2(div_pos(y[2 * i], s, rs), div_pos(y[2 * i + 1], s, rs)) << (16 * (i & 1));
+    } else if (s != 0.f) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) w[i / 2] |= cvt_e4m3x2(__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s)) << (16 * (i & 1));
+    }
+    if (kWide) {
+        *reinterpret_cast<uint2*>(dst + c0) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (c0 + i < C) dst[c0 + i] = (uint8_t)(w[i / 4] >> (8 * (i & 3)));
+    }
+}
+
+enum { kOutBf16 = 0, kOutRow = 1, kOutGroup = 2 };
+
+template <int kItems, bool kWarp, bool kWide, int kOut>
+__global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : 1024) k_rmsnorm(NormParams p) {
+    __shared__ float sh[2][32];
+    __shared__ double shd[32];
+    const int T = kWarp ? 32 : (int)blockDim.x, t = kWarp ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
+    const long long row = kWarp ? (long long)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : (long long)blockIdx.x;
+    if (kWarp && row >= p.rows) return;
+    const uint16_t* x = p.x + row * p.x_stride;
+    const uint16_t* r = p.residual + row * p.r_stride;
+    uint32_t xw[kItems][4], rw[kItems][4];
+#pragma unroll
+    for (int i = 0; i < kItems; i++) {
+        const int c0 = 8 * (t + i * T);
+        if (c0 < p.C) {
+            load8<kWide>(x, c0, p.C, xw[i]);
+            if (p.residual) load8<kWide>(r, c0, p.C, rw[i]);
+        }
+    }
+    float h[kItems][8], ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < kItems; i++) {
+        const int c0 = 8 * (t + i * T);
+#pragma unroll
+        for (int j = 0; j < 8; j++) h[i][j] = 0.f;
+        if (c0 >= p.C) continue;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            h[i][2 * j] = bf16_lo(xw[i][j]), h[i][2 * j + 1] = bf16_hi(xw[i][j]);
+            if (p.residual) h[i][2 * j] += bf16_lo(rw[i][j]), h[i][2 * j + 1] += bf16_hi(rw[i][j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++) ss = fmaf(h[i][j], h[i][j], ss);
+        if (p.sum) store8<kWide>(p.sum + row * p.s_stride, c0, p.C, h[i]);
+    }
+    ss = row_reduce<kWarp>(ss, sh[0], [](float a, float b) { return a + b; });
+    const float v = ss / (float)p.C + p.eps;
+    float inv = rsqrtf(v);
+    if (!(v > 0x1p-100f && v < 0x1p100f)) {
+        // squares beyond fp32's range (or not finite): the same formula in 64 bits
+        double sd = 0.0;
+#pragma unroll
+        for (int i = 0; i < kItems; i++)
+#pragma unroll
+            for (int j = 0; j < 8; j++) sd += (double)h[i][j] * h[i][j];
+        sd = row_reduce<kWarp>(sd, shd, [](double a, double b) { return a + b; });
+        const double id = 1.0 / sqrt(sd / p.C + (double)p.eps);
+#pragma unroll
+        for (int i = 0; i < kItems; i++)
+#pragma unroll
+            for (int j = 0; j < 8; j++) h[i][j] = (float)(h[i][j] * id);
+        inv = 1.f;
+    }
+    float am = 0.f;
+#pragma unroll
+    for (int i = 0; i < kItems; i++) {
+        const int c0 = 8 * (t + i * T);
+        if (c0 < p.C) {
+            uint32_t gw[4];
+            if (p.gamma) load8<kWide>(p.gamma, c0, p.C, gw);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                h[i][j] *= inv;
+                if (p.gamma) h[i][j] *= (j & 1) ? bf16_hi(gw[j / 2]) : bf16_lo(gw[j / 2]);
+            }
+            if (!kWide) {   // channels past the row's end take no part in a maximum (0 times infinity)
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    if (c0 + j >= p.C) h[i][j] = 0.f;
+            }
+        }
+        if (kOut == kOutBf16) {
+            if (c0 < p.C) store8<kWide>((uint16_t*)p.y + row * p.y_stride, c0, p.C, h[i]);
+        } else {
+            float a = fabsf(h[i][0]);
+#pragma unroll
+            for (int j = 1; j < 8; j++) a = max_nan(a, fabsf(h[i][j]));
+            if (kOut == kOutRow) {
+                am = max_nan(am, a);
+            } else {
+                // 64 channels sit in eight neighbouring lanes
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
+                const float s = a / 448.0f;
+                if (c0 < p.C) {
+                    store_codes8<kWide>((uint8_t*)p.y + row * p.y_stride, c0, p.C, h[i], s);
+                    if ((t & 7) == 0) p.scales[row * ((p.C + 63) / 64) + c0 / 64] = s;
+                }
+            }
+        }
+    }
+    if (kOut == kOutRow) {
+        const float s = row_reduce<kWarp>(am, sh[1], max_nan) / 448.0f;
+#pragma unroll
+        for (int i = 0; i < kItems; i++) {
+            const int c0 = 8 * (t + i * T);
+            if (c0 < p.C) store_codes8<kWide>((uint8_t*)p.y + row * p.y_stride, c0, p.C, h[i], s);
+        }
+        if (t == 0) p.scales[row] = s;
+    }
+}
+
+template <int kItems, bool kWarp, bool kWide>
+void launch(const NormParams& p, unsigned grid, unsigned threads, cudaStream_t st) {
+    if (!p.scales)
+        k_rmsnorm<kItems, kWarp, kWide, kOutBf16><<<grid, threads, 0, st>>>(p);
+    else if (!p.group)
+        k_rmsnorm<kItems, kWarp, kWide, kOutRow><<<grid, threads, 0, st>>>(p);
+    else
+        k_rmsnorm<kItems, kWarp, kWide, kOutGroup><<<grid, threads, 0, st>>>(p);
+}
+
+template <bool kWide>
+void launch_width(const NormParams& p, cudaStream_t st) {
+    const int pieces = (int)cdiv(p.C, 8);
+    const unsigned warp_grid = (unsigned)cdiv(p.rows, kWarpRows);
+    if (pieces <= 32) return launch<1, true, kWide>(p, warp_grid, 32 * kWarpRows, st);
+    if (pieces <= 64) return launch<2, true, kWide>(p, warp_grid, 32 * kWarpRows, st);
+    if (pieces <= 128) return launch<4, true, kWide>(p, warp_grid, 32 * kWarpRows, st);
+    const int items = pieces <= 256 ? 1 : pieces <= 1024 ? 2 : kMaxItems;
+    const unsigned threads = (unsigned)(cdiv(cdiv(pieces, items), 32) * 32);
+    if (items == 1) return launch<1, false, kWide>(p, (unsigned)p.rows, threads, st);
+    if (items == 2) return launch<2, false, kWide>(p, (unsigned)p.rows, threads, st);
+    launch<kMaxItems, false, kWide>(p, (unsigned)p.rows, threads, st);
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm(const NormParams& p, cudaStream_t st) {
+    auto wide = [](const void* q, long long stride, int bytes) {
+        return ((uintptr_t)q & (bytes - 1)) == 0 && stride * (bytes / 8) % bytes == 0;
+    };
+    // 16-byte pieces (8 bytes for codes) need every row of every buffer on that boundary
+    const bool w = p.C % 8 == 0 && wide(p.x, p.x_stride, 16) && wide(p.residual, p.residual ? p.r_stride : 0, 16) &&
+                   wide(p.gamma, 0, 16) && wide(p.sum, p.sum ? p.s_stride : 0, 16) &&
+                   wide(p.y, p.y_stride, p.scales ? 8 : 16);
+    if (w)
+        launch_width<true>(p, st);
+    else
+        launch_width<false>(p, st);
+    return cudaGetLastError();
+}
+
+}  // namespace dq
