@@ -113,6 +113,22 @@ bool map_sfb(CUtensorMap* m, const void* base, int cols, int Co, int blocks = 4)
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 4-D map over one copy of each scale in the B-operand scale layout (dq_sfb_offset): dim 0 the 128
+// bytes of eight lanes of one half of a 256-row tile, dim 1 the halves, dim 2 the four groups of
+// eight lanes of the first lane quadrant (the other three hold the same bytes), dim 3 the 4096-byte
+// blocks.  A box is the scales of 128 rows and 256 channels, 512 bytes for each 64-channel block.
+bool map_sfb_lanes(CUtensorMap* m, const void* base, int cols, int Co) {
+    EncodeTiledFn f = encode_fn();
+    if (!f) return false;
+    cuuint64_t dims[4] = {128, 2, 4, (cuuint64_t)cols / 64 * (Co / 256)};
+    cuuint64_t strides[3] = {128, 256, 4096};
+    cuuint32_t box[4] = {128, 1, 4, 4};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool aligned(const void* p) { return ((uintptr_t)p & 255u) == 0; }
 
 // Text of the last CUDA runtime error an entry point of this thread returned DQ_ERR_CUDA for.
@@ -849,7 +865,7 @@ int dq_rows_workspace_bytes(int rows, int Ci, int Co, int rank, size_t* bytes) {
     if (!bytes) return DQ_ERR_INVALID_ARG;
     const int rc = check_rows_shape(rows, Ci, Co, rank);
     if (rc) return rc;
-    *bytes = dq::rows_layout(rows, rank).total;
+    *bytes = dq::rows_layout(rows, Ci, rank).total;
     return DQ_OK;
 }
 
@@ -870,8 +886,9 @@ int dq_rows_forward(const void* X, int x_format, long long x_stride, const float
     if (((uintptr_t)X & 15) || x_stride % (codes ? 16 : 8) || ((uintptr_t)x_scales & 3) || ((uintptr_t)Y & 1))
         return DQ_ERR_ALIGNMENT;
     if (!aligned(packed_W) || !aligned(L1_mma) || !aligned(L2_slab) || !aligned(workspace)) return DQ_ERR_ALIGNMENT;
-    const dq::RowsLayout wl = dq::rows_layout(rows, rank);
+    const dq::RowsLayout wl = dq::rows_layout(rows, Ci, rank);
     if (workspace_bytes < wl.total) return DQ_ERR_WORKSPACE_TOO_SMALL;
+    if (!encode_fn()) return DQ_ERR_NO_DEVICE;
     const dq::PackedLayout pl = dq::packed_layout(Co, Ci, rank);
     uint8_t* ws = (uint8_t*)workspace;
     dq::RowsParams p;
@@ -895,9 +912,21 @@ int dq_rows_forward(const void* X, int x_format, long long x_stride, const float
     p.l2 = (const uint16_t*)L2_slab;
     p.y = (uint16_t*)Y;
     p.status = (int*)(ws + wl.off_status);
-    p.u = (float*)(ws + wl.off_u);
+    p.e = (float*)(ws + wl.off_e);
+    p.u = (uint16_t*)(ws + wl.off_u);
+    p.xh = (uint16_t*)(ws + wl.off_xh);
+    p.hilo = x_format == DQ_ROWS_E4M3_GROUP64;
     p.budget_ns = kWaitBudgetNs;
-    cudaError_t e = dq::launch_rows(p, (cudaStream_t)stream);
+    dq::rows_plan(p);
+    CUtensorMap tm_w, tm_s, tm_x, tm_l2, tm_u;
+    if (!map_2d(&tm_w, p.packed_w + pl.off_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Ci / 2, Co, 128, 128))
+        return map_fail("weight codes");
+    if (!map_sfb_lanes(&tm_s, p.packed_w + pl.off_scales, Ci, Co)) return map_fail("weight scales");
+    if (!map_2d(&tm_x, p.xh, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p.hilo ? 2 * Ci : Ci, rows, 64, p.n_pad))
+        return map_fail("rows");
+    if (!map_2d(&tm_l2, L2_slab, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pl.slab, Co, 64, 128)) return map_fail("L2");
+    if (!map_2d(&tm_u, p.u, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pl.slab, rows, 64, p.n_pad)) return map_fail("U");
+    cudaError_t e = dq::launch_rows(tm_w, tm_s, tm_x, tm_l2, tm_u, p, (cudaStream_t)stream);
     return e == cudaSuccess ? DQ_OK : cuda_fail(e, "few-row product");
 }
 

@@ -228,16 +228,19 @@ DQ_HD WsLayout ws_layout(const Geom& g, int Ci, int Co, int rank, int kgroup = 0
     return L;
 }
 
-// Workspace of dq_rows_forward: the status word, then U = X L1 (rows x rank fp32).
+// Workspace of dq_rows_forward: the status word, the rows' factors (fp32), U as BF16 hi + lo (rows x
+// slab) and the rows as FP16 (rows x 2 Ci: a scale per 64 channels keeps hi and lo halves).
 struct RowsLayout {
-    size_t total, off_status, off_u;
+    size_t total, off_status, off_e, off_u, off_xh;
 };
 
-DQ_HD RowsLayout rows_layout(int rows, int rank) {
+DQ_HD RowsLayout rows_layout(int rows, int Ci, int rank) {
     RowsLayout L;
     size_t off = 0;
     L.off_status = off;  off = align_up(off + 16, kAlign);
-    L.off_u = off;       off = align_up(off + (size_t)rows * rank * 4, kAlign);
+    L.off_e = off;       off = align_up(off + (size_t)rows * 4, kAlign);
+    L.off_u = off;       off = align_up(off + (size_t)rows * slab_width(rank) * 2, kAlign);
+    L.off_xh = off;      off = align_up(off + (size_t)rows * Ci * 4, kAlign);
     L.total = off;
     return L;
 }

@@ -133,10 +133,19 @@ struct RowsParams {
     const uint16_t* l2;         // Co x slab
     uint16_t* y;
     int* status;
-    float* u;                   // rows x rank
+    float* e;                   // rows: factor of each row of xh
+    uint16_t* xh;               // rows x Ci FP16 (rows x 2 Ci with hilo): the product's B operand
+    uint16_t* u;                // rows x slab BF16: X L1 / (e S_W) as hi + lo
+    int hilo;                   // xh holds hi and lo halves (a scale per 64 channels)
     uint64_t budget_ns;
+    // the cut of the product (rows_plan)
+    int n_rows, n_pad, passes;  // rows of X per pass, that rounded up to 16
+    int splits;                 // parts of the channels, one cluster per tile
+    int stages_a, stages_b, ring, smem, tmem_cols, d_cols;
 };
-cudaError_t launch_rows(const RowsParams& p, cudaStream_t st);
+void rows_plan(RowsParams& p);
+cudaError_t launch_rows(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const CUtensorMap& tm_x,
+                        const CUtensorMap& tm_l2, const CUtensorMap& tm_u, const RowsParams& p, cudaStream_t st);
 
 // Device address of the no-allocation entry point's fixed workspace on the
 // current device (dq_noalloc.cu); a dq_status code.

@@ -1,13 +1,127 @@
 // The product of few rows with a packed 4-bit weight (dq_rows_forward):
 //   Y[m] = act( S_W sum_c xv[m][c] (q s_b)[o][c] + (xv[m] L1) L2 + b )
+//
+// With few rows the weight's bytes bound it: they cross from HBM once, and
+// everything else hides behind that.  Two launches:
+//
+//   k_rows_prepare  rows -> the B operand, and U = xv L1.  FP16 holds every
+//     q s_b exactly (6 significant bits, 2^-10 to 2688), so the product runs on
+//     kind::f16 with FP16 operands, and a BF16 row is moved into FP16's range
+//     by a power of two E of its own: x / E <= 2^15 keeps all 8 bits of values
+//     down to 2^-29 of the row's largest, and is off by at most 2^-40 of the
+//     largest below that, far under the fp32 sums' rounding.  E4M3 codes are
+//     FP16 values already (E = the row's scale); with a scale per 64 channels
+//     the row is code * scale, split into FP16 hi + lo (22 bits).  A cluster of
+//     eight CTAs takes 16 rows, an eighth of the channels each, and joins its
+//     maxima and its partial sums of U in a fixed order through distributed
+//     shared memory; U / (E S_W) is kept as BF16 hi + lo, as in the cube layer.
+//   k_rows_main     the product.  A CTA owns 128 output channels (the MMA's
+//     rows) and up to 256 rows of X (its columns), and a part of the channels
+//     when the tiles alone do not fill the GPU: the CTAs of a tile form a
+//     cluster and sum their parts in rank order.  Codes and scales arrive by
+//     TMA; eight warps turn them into FP16 (cvt.f16x2.e2m1x2, one product with
+//     the group's scale) and put them into tensor memory, the MMA's A operand:
+//     through shared memory they would cross it three times (write, and the
+//     MMA's reads), which alone would take longer than the weight takes from
+//     HBM.  The low-rank factor is extra BF16 K steps on the same accumulator.
+//     The weight's loads do not wait for k_rows_prepare (programmatic launch).
 #include "../../include/deltaquant.h"
 #include "dq_common.h"
 #include "dq_internal.h"
 #include "dq_ptx.cuh"
 
+#include <atomic>
+
 namespace dq {
 
 namespace {
+
+// ------------------------------------------------------------------ PTX used by this file alone
+
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t cluster_addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_dsmem_f32(uint32_t cluster_addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+}
+
+// D(16 x 8) += A(16 x 16) B(16 x 8), BF16 operands, fp32 sums
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// kind::f16, FP16 x FP16 -> fp32, K-major operands
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// Two E4M3 codes -> FP16 pair (exact), the low byte's in the low half
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)codes));
+    return h2;
+}
+
+// Eight E2M1 codes (value 2i in the low nibble of byte i) times the FP16 pair s -> four FP16 pairs
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t s, uint32_t* out) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        ".reg .b32 t0, t1, t2, t3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 t0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 t1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 t2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 t3, b3;\n\t"
+        "mul.rn.f16x2 %0, t0, %5;\n\t"
+        "mul.rn.f16x2 %1, t1, %5;\n\t"
+        "mul.rn.f16x2 %2, t2, %5;\n\t"
+        "mul.rn.f16x2 %3, t3, %5;\n\t}"
+        : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3])
+        : "r"(w), "r"(s));
+}
+
+__device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// 2^e for -126 <= e <= 127
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
 __device__ __forceinline__ bool header_ok(const RowsParams& p) {
     const PackedHeader* h = reinterpret_cast<const PackedHeader*>(p.packed_w);
@@ -15,65 +129,542 @@ __device__ __forceinline__ bool header_ok(const RowsParams& p) {
            h->rank == p.rank && h->slab == p.slab;
 }
 
-__device__ __forceinline__ float x_value(const RowsParams& p, int m, int c) {
-    if (p.x_format == DQ_ROWS_BF16) return bf16_lo(((const uint16_t*)p.x)[(long long)m * p.x_stride + c]);
-    const float v = e4m3_to_f32(((const uint8_t*)p.x)[(long long)m * p.x_stride + c]);
-    return v * (p.x_format == DQ_ROWS_E4M3 ? p.x_scales[m] : p.x_scales[(long long)m * (p.Ci / 64) + c / 64]);
+// ------------------------------------------------------------------ rows -> B operand and U
+
+constexpr int kPrepThreads = 256, kPrepWarps = 8, kPrepCluster = 8, kPrepRows = 16;
+
+// The power of two that moves a BF16 row (largest magnitude am > 0, finite) into FP16's range: am / 2^k
+// in [2^14, 2^15); a subnormal am is taken as 2^-126.
+__device__ __forceinline__ int row_exponent(float am) {
+    const int e = (int)((__float_as_uint(am) >> 23) & 255);
+    return (e ? e - 127 : -126) - 14;
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+// x 2^-k in two exact steps (k in [-140, 113])
+struct Scale2 {
+    float a, b;
+};
+__device__ __forceinline__ Scale2 inv_scale(int k) {
+    const int h = (-k) / 2;
+    return Scale2{pow2i(h), pow2i(-k - h)};
 }
 
-// U[m][j] = sum_c xv[m][c] L1[j][c]: one warp each
-__global__ void __launch_bounds__(256) k_rows_u(RowsParams p) {
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.status = header_ok(p) ? 0 : kStatusBadWeight;
-    const int m = blockIdx.x, j = blockIdx.y * 8 + (threadIdx.x >> 5);
-    float u = 0.f;
-    for (int c = threadIdx.x & 31; c < p.Ci; c += 32) u = fmaf(x_value(p, m, c), bf16_lo(p.l1[(long long)j * p.Ci + c]), u);
-    u = warp_sum(u);
-    if ((threadIdx.x & 31) == 0) p.u[(long long)m * p.rank + j] = u;
-}
+template <int kNT, int kFmt>
+__global__ void __launch_bounds__(kPrepThreads) k_rows_prepare(RowsParams p) {
+    extern __shared__ float prep_sm[];
+    // [8 warps][16][rank] partial sums, then [16][rank] of this CTA, [8][16] maxima, [16] of this CTA
+    float* wpart = prep_sm;
+    float* part = wpart + kPrepWarps * kPrepRows * p.rank;
+    float* wmax = part + kPrepRows * p.rank;
+    float* cmax = wmax + kPrepWarps * kPrepRows;
+    int* rexp = (int*)(cmax + kPrepRows);       // [16] exponents k
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int crank = (int)cluster_ctarank();
+    const int m0 = (int)(blockIdx.x / kPrepCluster) * kPrepRows;
+    const int nm = imin(kPrepRows, p.rows - m0);
+    const int nblk = p.Ci / 64, b0 = nblk * crank / kPrepCluster, b1 = nblk * (crank + 1) / kPrepCluster;
+    griddep_launch();
+    if (blockIdx.x == 0 && tid == 0) *p.status = header_ok(p) ? 0 : kStatusBadWeight;
+    const float S_W = reinterpret_cast<const PackedHeader*>(p.packed_w)->S_W;
 
-// One output value per warp
-__global__ void __launch_bounds__(256) k_rows_simple(RowsParams p) {
-    if (!header_ok(p)) return;
-    const int o = blockIdx.x * 8 + (threadIdx.x >> 5), m = blockIdx.y, lane = threadIdx.x & 31;
-    const uint8_t* codes = p.packed_w + p.off_codes + (long long)o * (p.Ci / 2);
-    float acc = 0.f;
-    for (int b = lane; b < p.Ci / 16; b += 32) {
-        const float s = e4m3_to_f32(p.packed_w[p.off_scales + sfb_offset(o, b, p.Ci)]);
-        float part = 0.f;
-        for (int i = 0; i < 16; i++) {
-            const int q = (codes[b * 8 + i / 2] >> (4 * (i & 1))) & 15, e = (q >> 1) & 3;
-            const float mag = e ? (1.f + 0.5f * (q & 1)) * (float)(1 << e) * 0.5f : 0.5f * (q & 1);
-            part = fmaf(x_value(p, m, b * 16 + i), q & 8 ? -mag : mag, part);
+    // X L1 of this CTA's channels: a warp takes 64 channels at a time, lane t of a quad 16 of them (any
+    // assignment of channels to the MMA's k is right as long as both operands use it)
+    float acc[kNT][4];
+#pragma unroll
+    for (int n = 0; n < kNT; n++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) acc[n][i] = 0.f;
+    float am0 = 0.f, am1 = 0.f;
+    for (int b = b0 + warp; b < b1; b += kPrepWarps) {
+        uint32_t xa[2][8];   // rows g and g + 8: 16 channels as BF16 pairs
+        float sc0 = 0.f, sc1 = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int m = g + 8 * h;
+#pragma unroll
+            for (int i = 0; i < 8; i++) xa[h][i] = 0;
+            if (m < nm) {
+                const long long off = (long long)(m0 + m) * p.x_stride + b * 64 + t * 16;
+                if (kFmt == DQ_ROWS_BF16) {
+                    const uint4* src = reinterpret_cast<const uint4*>((const uint16_t*)p.x + off);
+                    const uint4 u = src[0], v = src[1];
+                    xa[h][0] = u.x, xa[h][1] = u.y, xa[h][2] = u.z, xa[h][3] = u.w;
+                    xa[h][4] = v.x, xa[h][5] = v.y, xa[h][6] = v.z, xa[h][7] = v.w;
+                } else {
+                    const uint4 u = *reinterpret_cast<const uint4*>((const uint8_t*)p.x + off);
+                    const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int i = 0; i < 8; i++) xa[h][i] = e4m3x2_to_bf16x2(q[i / 2] >> (16 * (i & 1)));
+                }
+                if (kFmt == DQ_ROWS_E4M3_GROUP64) (h ? sc1 : sc0) = p.x_scales[(long long)(m0 + m) * nblk + b];
+            }
+            if (kFmt != DQ_ROWS_E4M3) {
+                float a = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; i++) a = max_nan(a, max_nan(fabsf(bf16_lo(xa[h][i])), fabsf(bf16_hi(xa[h][i]))));
+                if (kFmt == DQ_ROWS_E4M3_GROUP64) a = fabsf(a * (h ? sc1 : sc0));
+                (h ? am1 : am0) = max_nan(h ? am1 : am0, a);
+            }
         }
-        acc = fmaf(part, s, acc);
+#pragma unroll
+        for (int n = 0; n < kNT; n++) {
+            if (8 * n >= p.rank) break;
+            const uint4* src = reinterpret_cast<const uint4*>(p.l1 + (long long)(8 * n + g) * p.Ci + b * 64 + t * 16);
+            const uint4 u = src[0], v = src[1];
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_16816(d, xa[0][0], xa[1][0], xa[0][1], xa[1][1], u.x, u.y);
+            mma_16816(d, xa[0][2], xa[1][2], xa[0][3], xa[1][3], u.z, u.w);
+            mma_16816(d, xa[0][4], xa[1][4], xa[0][5], xa[1][5], v.x, v.y);
+            mma_16816(d, xa[0][6], xa[1][6], xa[0][7], xa[1][7], v.z, v.w);
+            const float s0 = kFmt == DQ_ROWS_E4M3_GROUP64 ? sc0 : 1.f, s1 = kFmt == DQ_ROWS_E4M3_GROUP64 ? sc1 : 1.f;
+            acc[n][0] = fmaf(d[0], s0, acc[n][0]);
+            acc[n][1] = fmaf(d[1], s0, acc[n][1]);
+            acc[n][2] = fmaf(d[2], s1, acc[n][2]);
+            acc[n][3] = fmaf(d[3], s1, acc[n][3]);
+        }
     }
-    float low = 0.f;
-    for (int j = lane; j < p.rank; j += 32) low = fmaf(p.u[(long long)m * p.rank + j], bf16_lo(p.l2[(long long)o * p.slab + j]), low);
-    acc = warp_sum(acc);
-    low = warp_sum(low);
-    if (lane) return;
-    const PackedHeader* h = reinterpret_cast<const PackedHeader*>(p.packed_w);
-    float y = acc * h->S_W + low;
-    if (h->flags & kPackedHasBias) y += *(const float*)(p.packed_w + p.off_bias + 4ll * o);
-    if (p.gelu) {
-        float g, unused;
-        f2_unpack(gelu_erf2(f2_pack(y, 0.f)), g, unused);
-        y = g;
+    // lane (g, t) holds U of rows g, g + 8 and ranks 8 n + 2 t, + 1
+#pragma unroll
+    for (int n = 0; n < kNT; n++) {
+        if (8 * n >= p.rank) break;
+        float* w0 = wpart + (warp * kPrepRows + g) * p.rank + 8 * n + 2 * t;
+        w0[0] = acc[n][0], w0[1] = acc[n][1];
+        w0[8 * p.rank] = acc[n][2], w0[8 * p.rank + 1] = acc[n][3];
     }
-    p.y[(long long)m * p.y_stride + o] = f32_to_bf16_rn(y);
+    if (kFmt != DQ_ROWS_E4M3) {
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            am0 = max_nan(am0, __shfl_xor_sync(0xffffffffu, am0, o));
+            am1 = max_nan(am1, __shfl_xor_sync(0xffffffffu, am1, o));
+        }
+        if (t == 0) wmax[warp * kPrepRows + g] = am0, wmax[warp * kPrepRows + g + 8] = am1;
+    }
+    __syncthreads();
+    for (int e = tid; e < kPrepRows * p.rank; e += kPrepThreads) {
+        float s = 0.f;
+        for (int w = 0; w < kPrepWarps; w++) s += wpart[w * kPrepRows * p.rank + e];
+        part[e] = s;
+    }
+    if (kFmt != DQ_ROWS_E4M3 && tid < kPrepRows) {
+        float a = 0.f;
+        for (int w = 0; w < kPrepWarps; w++) a = max_nan(a, wmax[w * kPrepRows + tid]);
+        cmax[tid] = a;
+    }
+    cluster_sync();
+    // the row's factor E: the product's epilogue multiplies by it
+    if (tid < kPrepRows) {
+        int k = 0;
+        float E = 1.f;
+        if (kFmt == DQ_ROWS_E4M3) {
+            E = tid < nm ? p.x_scales[m0 + tid] : 0.f;
+        } else {
+            float a = 0.f;
+            for (int c = 0; c < kPrepCluster; c++) a = max_nan(a, ld_dsmem_f32(mapa_shared(smem_u32(&cmax[tid]), c)));
+            if (!(a < __int_as_float(0x7F800000))) {
+                E = __int_as_float(0x7FC00000);   // a NaN or an infinity in the row: NaN all over it
+            } else if (a > 0.f) {
+                k = row_exponent(a);
+                E = k >= -126 ? pow2i(k) : __int_as_float(1 << (k + 149));
+            }
+        }
+        rexp[tid] = k;
+        if (crank == 0 && tid < nm) p.e[m0 + tid] = E;
+    }
+    __syncthreads();
+    // U / (E S_W) as BF16 hi + lo, an eighth of the (row, rank) pairs per CTA; zeros up to the slab's width
+    for (int e = tid + crank * kPrepThreads; e < nm * p.rank; e += kPrepThreads * kPrepCluster) {
+        const int m = e / p.rank, j = e - m * p.rank;
+        const uint32_t at = smem_u32(&part[e]);
+        float u = 0.f;
+        for (int c = 0; c < kPrepCluster; c++) u += ld_dsmem_f32(mapa_shared(at, c));
+        const Scale2 s = inv_scale(rexp[m]);
+        u = u / S_W * s.a * s.b;
+        const float hi = bf16_lo(bf16x2_rn(u, 0.f));
+        uint16_t* dst = p.u + (long long)(m0 + m) * p.slab;
+        dst[j] = f32_to_bf16_rn(hi);
+        dst[p.rank + j] = f32_to_bf16_rn(u - hi);
+        for (int z = 2 * p.rank + j; z < p.slab; z += p.rank) dst[z] = 0;
+    }
+    // this CTA's channels as FP16
+    const int nv = (b1 - b0) * 8, ld = p.hilo ? 2 * p.Ci : p.Ci;
+    for (int i = tid; i < nm * nv; i += kPrepThreads) {
+        const int m = i / nv, c = b0 * 64 + (i - m * nv) * 8;
+        const long long off = (long long)(m0 + m) * p.x_stride + c;
+        uint16_t* dst = p.xh + (long long)(m0 + m) * ld + c;
+        uint32_t w[4];
+        if (kFmt == DQ_ROWS_E4M3) {
+            const uint2 q = *reinterpret_cast<const uint2*>((const uint8_t*)p.x + off);
+            w[0] = e4m3x2_to_f16x2(q.x), w[1] = e4m3x2_to_f16x2(q.x >> 16);
+            w[2] = e4m3x2_to_f16x2(q.y), w[3] = e4m3x2_to_f16x2(q.y >> 16);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            const Scale2 s = inv_scale(rexp[m]);
+            float v[8];
+            if (kFmt == DQ_ROWS_BF16) {
+                const uint4 q = *reinterpret_cast<const uint4*>((const uint16_t*)p.x + off);
+                const uint32_t r[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int j = 0; j < 4; j++) v[2 * j] = bf16_lo(r[j]), v[2 * j + 1] = bf16_hi(r[j]);
+            } else {
+                const uint2 q = *reinterpret_cast<const uint2*>((const uint8_t*)p.x + off);
+                const float gs = p.x_scales[(long long)(m0 + m) * nblk + c / 64];
+                const uint32_t r[2] = {q.x, q.y};
+#pragma unroll
+                for (int j = 0; j < 8; j++) v[j] = e4m3_to_f32(r[j / 4] >> (8 * (j & 3))) * gs;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[j] = v[j] * s.a * s.b;
+#pragma unroll
+            for (int j = 0; j < 4; j++) w[j] = f16x2_rn(v[2 * j], v[2 * j + 1]);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (kFmt == DQ_ROWS_E4M3_GROUP64) {
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    __half2_raw hr;
+                    hr.x = (uint16_t)(w[j] & 0xFFFFu), hr.y = (uint16_t)(w[j] >> 16);
+                    const float2 f = __half22float2(__half2(hr));
+                    w[j] = f16x2_rn(v[2 * j] - f.x, v[2 * j + 1] - f.y);
+                }
+                *reinterpret_cast<uint4*>(dst + p.Ci) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+    cluster_sync();   // no CTA leaves while another still reads its sums
+}
+
+// ------------------------------------------------------------------ the product
+
+constexpr int kMainThreads = 384;               // producers (A, B), MMA, a spare warp, eight decoding warps
+constexpr uint32_t kCodeBytes = 128 * 128;      // 128 output channels x 256 input channels
+constexpr uint32_t kScaleBytes = 4 * 512;
+constexpr uint32_t kStageA = kCodeBytes + kScaleBytes;
+constexpr int kMaxStages = 16;
+constexpr int kMaxSmem = 225 * 1024;             // dynamic shared memory of a CTA that has an SM to itself
+
+struct MainBars {
+    uint64_t fullA[kMaxStages], emptyA[kMaxStages], fullB[kMaxStages], emptyB[kMaxStages], tfull[8], tempty[8], accf;
+    uint32_t tmem;
+    int abort_flag;
+};
+
+__global__ void __launch_bounds__(kMainThreads, 2)
+    k_rows_main(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_s,
+                const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_l2,
+                const __grid_constant__ CUtensorMap tm_u, RowsParams p) {
+    extern __shared__ __align__(16) uint8_t rows_smem[];
+    uint8_t* sm = (uint8_t*)(((uintptr_t)rows_smem + 1023) & ~(uintptr_t)1023);
+    __shared__ MainBars bars;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int SA = p.stages_a, SB = p.stages_b, R = p.ring;
+    const uint32_t slotB = (uint32_t)p.n_pad * 128u;
+    uint8_t* ringB = sm + (size_t)SA * kStageA;
+    volatile int* abort_flag = &bars.abort_flag;
+    const int split = (int)blockIdx.x, splits = (int)gridDim.x;       // the cluster spans a tile's splits
+    const int o0 = (int)blockIdx.y * 128;
+    const int m0 = (int)blockIdx.z * p.n_rows;
+    const int nm = imin(p.n_rows, p.rows - m0);
+    const int k256 = p.Ci / 256, a0 = k256 * split / splits, nA = k256 * (split + 1) / splits - a0;
+    const int chunks = 4 * nA, tiles = p.hilo ? 2 : 1;
+    const int slabs = split == 0 ? p.slab / 64 : 0;
+
+    if (tid == 0) {
+        for (int s = 0; s < SA; s++) {
+            mbar_init(&bars.fullA[s], 1);
+            mbar_init(&bars.emptyA[s], 16);   // four chunks of a stage, four warps each
+        }
+        for (int s = 0; s < SB; s++) {
+            mbar_init(&bars.fullB[s], 1);
+            mbar_init(&bars.emptyB[s], 1);
+        }
+        for (int s = 0; s < R; s++) {
+            mbar_init(&bars.tfull[s], 4);
+            mbar_init(&bars.tempty[s], 1);
+        }
+        mbar_init(&bars.accf, 1);
+        bars.abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&bars.tmem, (uint32_t)p.tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem, ring0 = tmem + (uint32_t)p.d_cols;
+
+    if (warp == 0) {
+        // ------------------------------------------------ codes and scales, then the low-rank factor's rows
+        if (lane == 0) {
+            int g = 0;
+            const int total = nA + slabs;
+            for (; g < total; g++) {
+                const int s = g % SA;
+                if (g >= SA && !mbar_wait(&bars.emptyA[s], (uint32_t)(g / SA - 1) & 1, abort_flag, p.status, p.budget_ns)) break;
+                uint8_t* dst = sm + (size_t)s * kStageA;
+                if (g < nA) {
+                    mbar_arrive_expect_tx(&bars.fullA[s], kStageA);
+                    tma_load_2d(dst, &tm_w, &bars.fullA[s], (a0 + g) * 128, o0);
+                    // 32 lanes x 16 bytes per 64-channel block: half (o0 / 128) % 2 of the 256-row tile
+                    tma_load_4d(dst + kCodeBytes, &tm_s, &bars.fullA[s], 0, (o0 >> 7) & 1, 0,
+                                  (o0 >> 8) * (p.Ci / 64) + (a0 + g) * 4);
+                } else {
+                    mbar_arrive_expect_tx(&bars.fullA[s], kCodeBytes);
+                    tma_load_2d(dst, &tm_l2, &bars.fullA[s], (g - nA) * 64, o0);
+                }
+            }
+            for (int q = g > SA ? g - SA : 0; q < g; q++)   // every copy lands before shared memory is released
+                mbar_wait(&bars.fullA[q % SA], (uint32_t)(q / SA) & 1, abort_flag, nullptr, p.budget_ns, false);
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ------------------------------------------------ rows of X (FP16), then U
+        if (lane == 0) {
+            griddep_wait();
+            int g = 0;
+            const int main = chunks * tiles, total = main + slabs;
+            for (; g < total; g++) {
+                const int s = g % SB;
+                if (g >= SB && !mbar_wait(&bars.emptyB[s], (uint32_t)(g / SB - 1) & 1, abort_flag, p.status, p.budget_ns)) break;
+                mbar_arrive_expect_tx(&bars.fullB[s], slotB);
+                uint8_t* dst = ringB + (size_t)s * slotB;
+                if (g < main)
+                    tma_load_2d(dst, &tm_x, &bars.fullB[s], (g % tiles) * p.Ci + a0 * 256 + (g / tiles) * 64, m0);
+                else
+                    tma_load_2d(dst, &tm_u, &bars.fullB[s], (g - main) * 64, m0);
+            }
+            for (int q = g > SB ? g - SB : 0; q < g; q++)
+                mbar_wait(&bars.fullB[q % SB], (uint32_t)(q / SB) & 1, abort_flag, nullptr, p.budget_ns, false);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMAs
+        if (lane == 0) {
+            const uint32_t id_main = idesc_f16(128, p.n_pad), id_slab = idesc_bf16(128, p.n_pad);
+            int gb = 0;
+            bool alive = true;
+            for (int c = 0; alive && c < chunks; c++) {
+                const int slot = c % R;
+                if (!mbar_wait_spin(&bars.tfull[slot], (uint32_t)(c / R) & 1, abort_flag, p.status, p.budget_ns)) break;
+                for (int h = 0; h < tiles; h++, gb++) {
+                    const int s = gb % SB;
+                    if (!mbar_wait_spin(&bars.fullB[s], (uint32_t)(gb / SB) & 1, abort_flag, p.status, p.budget_ns)) {
+                        alive = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t bb = smem_u32(ringB + (size_t)s * slotB);
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        mma_f16_ts(tmem, ring0 + (uint32_t)(32 * slot + 8 * k), desc_k_sw128(bb + 32 * k), id_main,
+                                   (c | h | k) != 0);
+                    tc_commit(&bars.emptyB[s]);
+                }
+                if (alive) tc_commit(&bars.tempty[slot]);
+            }
+            for (int i = 0; alive && i < slabs; i++, gb++) {
+                const int s = gb % SB, ga = nA + i, sa = ga % SA;
+                if (!mbar_wait_spin(&bars.fullA[sa], (uint32_t)(ga / SA) & 1, abort_flag, p.status, p.budget_ns)) break;
+                if (!mbar_wait_spin(&bars.fullB[s], (uint32_t)(gb / SB) & 1, abort_flag, p.status, p.budget_ns)) break;
+                tc_fence_after();
+                const uint32_t aa = smem_u32(sm + (size_t)sa * kStageA), bb = smem_u32(ringB + (size_t)s * slotB);
+#pragma unroll
+                for (int k = 0; k < 4; k++) mma_bf16(tmem, desc_k_sw128(aa + 32 * k), desc_k_sw128(bb + 32 * k), id_slab, 1u);
+                tc_commit(&bars.emptyB[s]);
+            }
+            tc_commit(&bars.accf);
+            mbar_wait(&bars.accf, 0, abort_flag, nullptr, p.budget_ns, false);   // no MMA runs past this point
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ------------------------------------------------ codes -> FP16 in tensor memory
+        const int quad = warp & 3, group = (warp - 4) >> 2;   // 32 output channels; every other 64-channel chunk
+        const int row = quad * 32 + lane;
+        const uint32_t trow = ring0 + ((uint32_t)(quad * 32) << 16);
+        for (int c = group; c < chunks; c += 2) {
+            const int s = (c >> 2) % SA, slot = c % R;
+            if (!__all_sync(0xffffffffu, mbar_wait_spin(&bars.fullA[s], (uint32_t)((c >> 2) / SA) & 1, abort_flag, p.status,
+                                                        p.budget_ns)))
+                break;
+            // the TMA's 128-byte swizzle: 16-byte piece j of row r sits at piece j ^ (r % 8)
+            const uint8_t* st = sm + (size_t)s * kStageA;
+            const uint4 w0 = *reinterpret_cast<const uint4*>(st + row * 128 + (((2 * (c & 3)) ^ (row & 7)) << 4));
+            const uint4 w1 = *reinterpret_cast<const uint4*>(st + row * 128 + (((2 * (c & 3) + 1) ^ (row & 7)) << 4));
+            const uint32_t sw = *reinterpret_cast<const uint32_t*>(st + kCodeBytes + (c & 3) * 512 + lane * 16 + quad * 4);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.emptyA[s]);
+            const uint32_t s01 = e4m3x2_to_f16x2(sw), s23 = e4m3x2_to_f16x2(sw >> 16);
+            const uint32_t s0 = __byte_perm(s01, 0, 0x1010), s1 = __byte_perm(s01, 0, 0x3232);
+            const uint32_t s2 = __byte_perm(s23, 0, 0x1010), s3 = __byte_perm(s23, 0, 0x3232);
+            uint32_t v[16];
+            decode8(w0.x, s0, v), decode8(w0.y, s0, v + 4), decode8(w0.z, s1, v + 8), decode8(w0.w, s1, v + 12);
+            if (c >= R && !__all_sync(0xffffffffu, mbar_wait_spin(&bars.tempty[slot], (uint32_t)(c / R - 1) & 1, abort_flag,
+                                                                 p.status, p.budget_ns)))
+                break;
+            tc_fence_after();
+            tmem_st_x16(trow + (uint32_t)(32 * slot), v);
+            uint32_t u[16];
+            decode8(w1.x, s2, u), decode8(w1.y, s2, u + 4), decode8(w1.z, s3, u + 8), decode8(w1.w, s3, u + 12);
+            tmem_st_x16(trow + (uint32_t)(32 * slot + 16), u);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.tfull[slot]);
+        }
+        __syncwarp();
+    }
+
+    // ---------------------------------------------------- epilogue
+    const bool ok = header_ok(p);
+    const PackedHeader* hdr = reinterpret_cast<const PackedHeader*>(p.packed_w);
+    const float S_W = hdr->S_W;
+    const float* bias = (hdr->flags & kPackedHasBias) ? (const float*)(p.packed_w + p.off_bias) : nullptr;
+    bool done = true;
+    if (warp >= 4) {
+        done = __all_sync(0xffffffffu, mbar_wait_spin(&bars.accf, 0, abort_flag, p.status, p.budget_ns));
+        tc_fence_after();
+        griddep_wait();   // the rows' factors come from k_rows_prepare
+    }
+    const int quad = warp & 3, group = (warp - 4) >> 2, row = quad * 32 + lane;
+    // Y of one output channel and the rows m, m + 1 (the second where it exists)
+    auto finish = [&](int m, int o, float a0v, float a1v, float bv) {
+        const float e0 = p.e[m0 + m], e1 = m + 1 < nm ? p.e[m0 + m + 1] : 0.f;
+        float y0 = fmaf(a0v * S_W, e0, bv), y1 = fmaf(a1v * S_W, e1, bv);
+        if (p.gelu) f2_unpack(gelu_erf2(f2_pack(y0, y1)), y0, y1);
+        uint16_t* dst = p.y + (long long)(m0 + m) * p.y_stride + o;
+        dst[0] = f32_to_bf16_rn(y0);
+        if (m + 1 < nm) dst[p.y_stride] = f32_to_bf16_rn(y1);
+    };
+    if (splits == 1) {
+        if (warp >= 4 && done && ok) {
+            const float bv = bias ? bias[o0 + row] : 0.f;
+            for (int c = 16 * group; c < nm; c += 32) {
+                uint32_t acc[16];
+                tmem_ld_x16(tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)c, acc);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; j += 2)
+                    if (c + j < nm) finish(c + j, o0 + row, __uint_as_float(acc[j]), __uint_as_float(acc[j + 1]), bv);
+            }
+        }
+    } else {
+        // The parts of a tile: CTA r of the cluster sums, in rank order, the row pairs j with j % splits = r.
+        // The buffer takes the operand ring's place, so every CTA of the cluster is past its MMAs first.
+        __syncwarp();
+        cluster_sync();
+        float2* red = (float2*)sm;   // [source CTA][row pair / splits][128 output channels]
+        const int pairs = (nm + 1) / 2, own = (pairs + splits - 1) / splits;
+        if (warp >= 4 && done) {
+            for (int c = 16 * group; c < nm; c += 32) {
+                uint32_t acc[16];
+                tmem_ld_x16(tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)c, acc);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const int pr = c / 2 + j;
+                    if (pr < pairs) {
+                        const uint32_t at = mapa_shared(smem_u32(&red[(split * own + pr / splits) * 128 + row]), pr % splits);
+                        st_dsmem_f32(at, __uint_as_float(acc[2 * j]));
+                        st_dsmem_f32(at + 4, __uint_as_float(acc[2 * j + 1]));
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync();
+        if (warp >= 4 && done && ok) {
+            const int r = (tid - 128) & 127;
+            const float bv = bias ? bias[o0 + r] : 0.f;
+            for (int i = (tid - 128) >> 7; i * splits + split < pairs; i += 2) {
+                float a = 0.f, b = 0.f;
+                for (int q = 0; q < splits; q++) {
+                    const float2 v = red[(q * own + i) * 128 + r];
+                    a += v.x, b += v.y;
+                }
+                finish(2 * (i * splits + split), o0 + r, a, b, bv);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
+    }
+}
+
+template <int kNT>
+cudaError_t launch_prepare(const RowsParams& p, cudaStream_t st) {
+    const size_t smem = ((size_t)(kPrepWarps + 1) * kPrepRows * p.rank + (kPrepWarps + 2) * kPrepRows) * 4;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kPrepCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(cdiv(p.rows, kPrepRows) * kPrepCluster));
+    cfg.blockDim = dim3(kPrepThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto go = [&](auto kernel) {
+        if (smem > 48 * 1024) {
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+        }
+        return cudaLaunchKernelEx(&cfg, kernel, p);
+    };
+    if (p.x_format == DQ_ROWS_BF16) return go(k_rows_prepare<kNT, DQ_ROWS_BF16>);
+    if (p.x_format == DQ_ROWS_E4M3) return go(k_rows_prepare<kNT, DQ_ROWS_E4M3>);
+    return go(k_rows_prepare<kNT, DQ_ROWS_E4M3_GROUP64>);
 }
 
 }  // namespace
 
-cudaError_t launch_rows(const RowsParams& p, cudaStream_t st) {
-    k_rows_u<<<dim3(p.rows, p.rank / 8), 256, 0, st>>>(p);
-    k_rows_simple<<<dim3(p.Co / 8, p.rows), 256, 0, st>>>(p);
-    return cudaGetLastError();
+// How the product of `rows` rows is cut (RowsParams' fields from n_rows on).
+void rows_plan(RowsParams& p) {
+    // up to 256 rows of X a pass, evened out
+    const int passes = (int)cdiv(p.rows, 256);
+    p.n_rows = (int)cdiv(p.rows, passes);
+    p.n_pad = (int)cdiv(p.n_rows, 16) * 16;
+    p.passes = (int)cdiv(p.rows, p.n_rows);
+    const bool small = p.n_pad <= 64;   // two CTAs per SM: 256 tensor-memory columns and 113 KB each
+    p.tmem_cols = small ? 256 : 512;
+    p.d_cols = small ? 64 : 256;
+    p.ring = small ? 6 : 8;
+    const int slot = p.n_pad * 128, room = small ? 110 * 1024 : kMaxSmem - 1024;
+    p.stages_b = small ? (p.n_pad <= 16 ? 8 : p.n_pad <= 32 ? 6 : 4) : (p.n_pad <= 128 ? 6 : 4);
+    p.stages_a = imin(kMaxStages, (room - p.stages_b * slot) / (int)kStageA);
+    p.smem = p.stages_a * (int)kStageA + p.stages_b * slot + 1024;
+    // as many parts of the channels as still let every CTA be resident at once
+    const int tiles = p.Co / 128 * p.passes, places = small ? 296 : 148;
+    p.splits = 1;
+    while (p.splits < 8 && tiles * p.splits * 2 <= places && p.splits * 2 <= p.Ci / 256) p.splits *= 2;
+}
+
+cudaError_t launch_rows(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const CUtensorMap& tm_x, const CUtensorMap& tm_l2,
+                        const CUtensorMap& tm_u, const RowsParams& p, cudaStream_t st) {
+    cudaError_t e = p.rank <= 16   ? launch_prepare<2>(p, st)
+                    : p.rank <= 32 ? launch_prepare<4>(p, st)
+                    : p.rank <= 64 ? launch_prepare<8>(p, st)
+                                   : launch_prepare<16>(p, st);
+    if (e != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(k_rows_main, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem)) != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)p.splits, (unsigned)(p.Co / 128), (unsigned)p.passes);
+    cfg.blockDim = dim3(kMainThreads);
+    cfg.dynamicSmemBytes = (size_t)p.smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_rows_main, tm_w, tm_s, tm_x, tm_l2, tm_u, p);
 }
 
 }  // namespace dq
