@@ -341,6 +341,38 @@ constexpr uint32_t kStageA = kCodeBytes + kScaleBytes;
 constexpr int kMaxStages = 16;
 constexpr int kMaxSmem = 225 * 1024;             // dynamic shared memory of a CTA that has an SM to itself
 
+// A place in a ring and the parity of its use, stepped without a division (a division by a runtime
+// ring size costs more than a chunk's MMAs)
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int size) {
+        if (++slot == size) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// One lane's wait for the whole warp
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                          uint64_t budget_ns) {
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait_spin(bar, parity, abort_flag, status, budget_ns);
+    return __shfl_sync(0xffffffffu, ok, 0);
+}
+
+// One lane of a converged warp, the same every time
+__device__ __forceinline__ bool elect_one() {
+    uint32_t pred;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(pred));
+    return pred != 0;
+}
+
 struct MainBars {
     uint64_t fullA[kMaxStages], emptyA[kMaxStages], fullB[kMaxStages], emptyB[kMaxStages], tfull[8], tempty[8], accf;
     uint32_t tmem;
@@ -396,21 +428,21 @@ __global__ void __launch_bounds__(kMainThreads, 2)
     if (warp == 0) {
         // ------------------------------------------------ codes and scales, then the low-rank factor's rows
         if (lane == 0) {
+            const int total = nA + slabs, half = (o0 >> 7) & 1, blk0 = (o0 >> 8) * (p.Ci / 64) + a0 * 4;
+            Ring r;
             int g = 0;
-            const int total = nA + slabs;
-            for (; g < total; g++) {
-                const int s = g % SA;
-                if (g >= SA && !mbar_wait(&bars.emptyA[s], (uint32_t)(g / SA - 1) & 1, abort_flag, p.status, p.budget_ns)) break;
-                uint8_t* dst = sm + (size_t)s * kStageA;
+            for (; g < total; g++, r.next(SA)) {
+                uint64_t* full = &bars.fullA[r.slot];
+                if (g >= SA && !mbar_wait(&bars.emptyA[r.slot], r.phase ^ 1, abort_flag, p.status, p.budget_ns)) break;
+                uint8_t* dst = sm + (size_t)r.slot * kStageA;
                 if (g < nA) {
-                    mbar_arrive_expect_tx(&bars.fullA[s], kStageA);
-                    tma_load_2d(dst, &tm_w, &bars.fullA[s], (a0 + g) * 128, o0);
-                    // 32 lanes x 16 bytes per 64-channel block: half (o0 / 128) % 2 of the 256-row tile
-                    tma_load_4d(dst + kCodeBytes, &tm_s, &bars.fullA[s], 0, (o0 >> 7) & 1, 0,
-                                  (o0 >> 8) * (p.Ci / 64) + (a0 + g) * 4);
+                    mbar_arrive_expect_tx(full, kStageA);
+                    tma_load_2d(dst, &tm_w, full, (a0 + g) * 128, o0);
+                    // 32 lanes x 16 bytes per 64-channel block: one half of the 256-row tile
+                    tma_load_4d(dst + kCodeBytes, &tm_s, full, 0, half, 0, blk0 + 4 * g);
                 } else {
-                    mbar_arrive_expect_tx(&bars.fullA[s], kCodeBytes);
-                    tma_load_2d(dst, &tm_l2, &bars.fullA[s], (g - nA) * 64, o0);
+                    mbar_arrive_expect_tx(full, kCodeBytes);
+                    tma_load_2d(dst, &tm_l2, full, (g - nA) * 64, o0);
                 }
             }
             for (int q = g > SA ? g - SA : 0; q < g; q++)   // every copy lands before shared memory is released
@@ -421,57 +453,66 @@ __global__ void __launch_bounds__(kMainThreads, 2)
         // ------------------------------------------------ rows of X (FP16), then U
         if (lane == 0) {
             griddep_wait();
-            int g = 0;
             const int main = chunks * tiles, total = main + slabs;
-            for (; g < total; g++) {
-                const int s = g % SB;
-                if (g >= SB && !mbar_wait(&bars.emptyB[s], (uint32_t)(g / SB - 1) & 1, abort_flag, p.status, p.budget_ns)) break;
-                mbar_arrive_expect_tx(&bars.fullB[s], slotB);
-                uint8_t* dst = ringB + (size_t)s * slotB;
-                if (g < main)
-                    tma_load_2d(dst, &tm_x, &bars.fullB[s], (g % tiles) * p.Ci + a0 * 256 + (g / tiles) * 64, m0);
-                else
-                    tma_load_2d(dst, &tm_u, &bars.fullB[s], (g - main) * 64, m0);
+            int x = a0 * 256, low = 0;
+            Ring r;
+            int g = 0;
+            for (; g < total; g++, r.next(SB)) {
+                uint64_t* full = &bars.fullB[r.slot];
+                if (g >= SB && !mbar_wait(&bars.emptyB[r.slot], r.phase ^ 1, abort_flag, p.status, p.budget_ns)) break;
+                mbar_arrive_expect_tx(full, slotB);
+                uint8_t* dst = ringB + (size_t)r.slot * slotB;
+                if (g < main) {
+                    tma_load_2d(dst, &tm_x, full, low + x, m0);
+                    low = tiles == 2 && low == 0 ? p.Ci : 0;   // hi, then lo of the same channels
+                    if (low == 0) x += 64;
+                } else {
+                    tma_load_2d(dst, &tm_u, full, (g - main) * 64, m0);
+                }
             }
             for (int q = g > SB ? g - SB : 0; q < g; q++)
                 mbar_wait(&bars.fullB[q % SB], (uint32_t)(q / SB) & 1, abort_flag, nullptr, p.budget_ns, false);
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ------------------------------------------------ MMAs
-        if (lane == 0) {
-            const uint32_t id_main = idesc_f16(128, p.n_pad), id_slab = idesc_bf16(128, p.n_pad);
-            int gb = 0;
-            bool alive = true;
-            for (int c = 0; alive && c < chunks; c++) {
-                const int slot = c % R;
-                if (!mbar_wait_spin(&bars.tfull[slot], (uint32_t)(c / R) & 1, abort_flag, p.status, p.budget_ns)) break;
-                for (int h = 0; h < tiles; h++, gb++) {
-                    const int s = gb % SB;
-                    if (!mbar_wait_spin(&bars.fullB[s], (uint32_t)(gb / SB) & 1, abort_flag, p.status, p.budget_ns)) {
-                        alive = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t bb = smem_u32(ringB + (size_t)s * slotB);
-#pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        mma_f16_ts(tmem, ring0 + (uint32_t)(32 * slot + 8 * k), desc_k_sw128(bb + 32 * k), id_main,
-                                   (c | h | k) != 0);
-                    tc_commit(&bars.emptyB[s]);
-                }
-                if (alive) tc_commit(&bars.tempty[slot]);
-            }
-            for (int i = 0; alive && i < slabs; i++, gb++) {
-                const int s = gb % SB, ga = nA + i, sa = ga % SA;
-                if (!mbar_wait_spin(&bars.fullA[sa], (uint32_t)(ga / SA) & 1, abort_flag, p.status, p.budget_ns)) break;
-                if (!mbar_wait_spin(&bars.fullB[s], (uint32_t)(gb / SB) & 1, abort_flag, p.status, p.budget_ns)) break;
+        // ------------------------------------------------ MMAs (one elected lane; the warp's control flow is uniform)
+        const uint32_t id_main = idesc_f16(128, p.n_pad), id_slab = idesc_bf16(128, p.n_pad);
+        const uint64_t bdesc0 = desc_k_sw128(smem_u32(ringB));
+        Ring rt, rb;
+        bool alive = true;
+        for (int c = 0; alive && c < chunks; c++, rt.next(R)) {
+            if (!(alive = warp_wait(&bars.tfull[rt.slot], rt.phase, abort_flag, p.status, p.budget_ns))) break;
+            const uint32_t at = ring0 + (uint32_t)(32 * rt.slot);
+            for (int h = 0; h < tiles; h++, rb.next(SB)) {
+                if (!(alive = warp_wait(&bars.fullB[rb.slot], rb.phase, abort_flag, p.status, p.budget_ns))) break;
                 tc_fence_after();
-                const uint32_t aa = smem_u32(sm + (size_t)sa * kStageA), bb = smem_u32(ringB + (size_t)s * slotB);
-#pragma unroll
-                for (int k = 0; k < 4; k++) mma_bf16(tmem, desc_k_sw128(aa + 32 * k), desc_k_sw128(bb + 32 * k), id_slab, 1u);
-                tc_commit(&bars.emptyB[s]);
+                const uint64_t bd = bdesc0 + (uint64_t)((uint32_t)rb.slot * (slotB >> 4));
+                if (elect_one()) {
+                    mma_f16_ts(tmem, at, bd, id_main, (c | h) != 0);
+                    mma_f16_ts(tmem, at + 8, bd + 2, id_main, 1u);
+                    mma_f16_ts(tmem, at + 16, bd + 4, id_main, 1u);
+                    mma_f16_ts(tmem, at + 24, bd + 6, id_main, 1u);
+                    tc_commit(&bars.emptyB[rb.slot]);
+                    if (h + 1 == tiles) tc_commit(&bars.tempty[rt.slot]);
+                }
+                __syncwarp();
             }
+        }
+        for (int i = 0; alive && i < slabs; i++, rb.next(SB)) {
+            const int ga = nA + i, sa = ga % SA;
+            if (!warp_wait(&bars.fullA[sa], (uint32_t)(ga / SA) & 1, abort_flag, p.status, p.budget_ns)) break;
+            if (!warp_wait(&bars.fullB[rb.slot], rb.phase, abort_flag, p.status, p.budget_ns)) break;
+            tc_fence_after();
+            const uint64_t ad = desc_k_sw128(smem_u32(sm + (size_t)sa * kStageA));
+            const uint64_t bd = bdesc0 + (uint64_t)((uint32_t)rb.slot * (slotB >> 4));
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 4; k++) mma_bf16(tmem, ad + 2 * k, bd + 2 * k, id_slab, 1u);
+                tc_commit(&bars.emptyB[rb.slot]);
+            }
+            __syncwarp();
+        }
+        if (elect_one()) {
             tc_commit(&bars.accf);
             mbar_wait(&bars.accf, 0, abort_flag, nullptr, p.budget_ns, false);   // no MMA runs past this point
         }
@@ -481,35 +522,37 @@ __global__ void __launch_bounds__(kMainThreads, 2)
         const int quad = warp & 3, group = (warp - 4) >> 2;   // 32 output channels; every other 64-channel chunk
         const int row = quad * 32 + lane;
         const uint32_t trow = ring0 + ((uint32_t)(quad * 32) << 16);
+        // the TMA's 128-byte swizzle: 16-byte piece j of row r sits at piece j ^ (r % 8)
+        const uint32_t at = (uint32_t)row * 128, x16 = (uint32_t)(row & 7);
+        Ring ra, rt;
+        rt.slot = group;   // the ring's size is even: a group keeps to its places
         for (int c = group; c < chunks; c += 2) {
-            const int s = (c >> 2) % SA, slot = c % R;
-            if (!__all_sync(0xffffffffu, mbar_wait_spin(&bars.fullA[s], (uint32_t)((c >> 2) / SA) & 1, abort_flag, p.status,
-                                                        p.budget_ns)))
-                break;
-            // the TMA's 128-byte swizzle: 16-byte piece j of row r sits at piece j ^ (r % 8)
-            const uint8_t* st = sm + (size_t)s * kStageA;
-            const uint4 w0 = *reinterpret_cast<const uint4*>(st + row * 128 + (((2 * (c & 3)) ^ (row & 7)) << 4));
-            const uint4 w1 = *reinterpret_cast<const uint4*>(st + row * 128 + (((2 * (c & 3) + 1) ^ (row & 7)) << 4));
+            if (!warp_wait(&bars.fullA[ra.slot], ra.phase, abort_flag, p.status, p.budget_ns)) break;
+            const uint8_t* st = sm + (size_t)ra.slot * kStageA;
+            const uint32_t j0 = 2 * (c & 3);
+            const uint4 w0 = *reinterpret_cast<const uint4*>(st + at + ((j0 ^ x16) << 4));
+            const uint4 w1 = *reinterpret_cast<const uint4*>(st + at + (((j0 + 1) ^ x16) << 4));
             const uint32_t sw = *reinterpret_cast<const uint32_t*>(st + kCodeBytes + (c & 3) * 512 + lane * 16 + quad * 4);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.emptyA[s]);
+            if (lane == 0) mbar_arrive(&bars.emptyA[ra.slot]);
             const uint32_t s01 = e4m3x2_to_f16x2(sw), s23 = e4m3x2_to_f16x2(sw >> 16);
             const uint32_t s0 = __byte_perm(s01, 0, 0x1010), s1 = __byte_perm(s01, 0, 0x3232);
             const uint32_t s2 = __byte_perm(s23, 0, 0x1010), s3 = __byte_perm(s23, 0, 0x3232);
             uint32_t v[16];
             decode8(w0.x, s0, v), decode8(w0.y, s0, v + 4), decode8(w0.z, s1, v + 8), decode8(w0.w, s1, v + 12);
-            if (c >= R && !__all_sync(0xffffffffu, mbar_wait_spin(&bars.tempty[slot], (uint32_t)(c / R - 1) & 1, abort_flag,
-                                                                 p.status, p.budget_ns)))
-                break;
+            if (c >= R && !warp_wait(&bars.tempty[rt.slot], rt.phase ^ 1, abort_flag, p.status, p.budget_ns)) break;
             tc_fence_after();
-            tmem_st_x16(trow + (uint32_t)(32 * slot), v);
+            tmem_st_x16(trow + (uint32_t)(32 * rt.slot), v);
             uint32_t u[16];
             decode8(w1.x, s2, u), decode8(w1.y, s2, u + 4), decode8(w1.z, s3, u + 8), decode8(w1.w, s3, u + 12);
-            tmem_st_x16(trow + (uint32_t)(32 * slot + 16), u);
+            tmem_st_x16(trow + (uint32_t)(32 * rt.slot + 16), u);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.tfull[slot]);
+            if (lane == 0) mbar_arrive(&bars.tfull[rt.slot]);
+            if ((c & 3) >= 2) ra.next(SA);
+            rt.slot += 2;
+            if (rt.slot >= R) rt.slot = group, rt.phase ^= 1;
         }
         __syncwarp();
     }
@@ -521,7 +564,7 @@ __global__ void __launch_bounds__(kMainThreads, 2)
     const float* bias = (hdr->flags & kPackedHasBias) ? (const float*)(p.packed_w + p.off_bias) : nullptr;
     bool done = true;
     if (warp >= 4) {
-        done = __all_sync(0xffffffffu, mbar_wait_spin(&bars.accf, 0, abort_flag, p.status, p.budget_ns));
+        done = warp_wait(&bars.accf, 0, abort_flag, p.status, p.budget_ns);
         tc_fence_after();
         griddep_wait();   // the rows' factors come from k_rows_prepare
     }
