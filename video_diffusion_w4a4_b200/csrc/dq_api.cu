@@ -917,6 +917,12 @@ int dq_rows_forward(const void* X, int x_format, long long x_stride, const float
     p.xh = (uint16_t*)(ws + wl.off_xh);
     p.hilo = x_format == DQ_ROWS_E4M3_GROUP64;
     p.budget_ns = kWaitBudgetNs;
+    if (rows <= dq::kRowsDirect) {
+        p.u_part = (float*)(ws + wl.off_u);
+        p.u_parts = dq::imin(dq::kRowsParts, Ci / 64);
+        cudaError_t e = dq::launch_rows_direct(p, (cudaStream_t)stream);
+        return e == cudaSuccess ? DQ_OK : cuda_fail(e, "few-row product");
+    }
     dq::rows_plan(p);
     CUtensorMap tm_w, tm_s, tm_x, tm_l2, tm_u;
     if (!map_2d(&tm_w, p.packed_w + pl.off_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Ci / 2, Co, 128, 128))

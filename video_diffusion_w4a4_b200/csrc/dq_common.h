@@ -229,7 +229,10 @@ DQ_HD WsLayout ws_layout(const Geom& g, int Ci, int Co, int rank, int kgroup = 0
 }
 
 // Workspace of dq_rows_forward: the status word, the rows' factors (fp32), U as BF16 hi + lo (rows x
-// slab) and the rows as FP16 (rows x 2 Ci: a scale per 64 channels keeps hi and lo halves).
+// slab) and the rows as FP16 (rows x 2 Ci: a scale per 64 channels keeps hi and lo halves); the smallest
+// calls keep partial sums of U in the place of the last two.
+constexpr int kRowsParts = 16;   // partial sums of U at most
+
 struct RowsLayout {
     size_t total, off_status, off_e, off_u, off_xh;
 };
@@ -241,7 +244,8 @@ DQ_HD RowsLayout rows_layout(int rows, int Ci, int rank) {
     L.off_e = off;       off = align_up(off + (size_t)rows * 4, kAlign);
     L.off_u = off;       off = align_up(off + (size_t)rows * slab_width(rank) * 2, kAlign);
     L.off_xh = off;      off = align_up(off + (size_t)rows * Ci * 4, kAlign);
-    L.total = off;
+    const size_t parts = align_up(L.off_u + (size_t)kRowsParts * rows * rank * 4, kAlign);
+    L.total = off > parts ? off : parts;
     return L;
 }
 

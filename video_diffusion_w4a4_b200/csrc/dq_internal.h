@@ -136,6 +136,8 @@ struct RowsParams {
     float* e;                   // rows: factor of each row of xh
     uint16_t* xh;               // rows x Ci FP16 (rows x 2 Ci with hilo): the product's B operand
     uint16_t* u;                // rows x slab BF16: X L1 / (e S_W) as hi + lo
+    float* u_part;              // up to kRowsDirect rows: u_parts x rows x rank partial sums of X L1
+    int u_parts;
     int hilo;                   // xh holds hi and lo halves (a scale per 64 channels)
     uint64_t budget_ns;
     // the cut of the product (rows_plan)
@@ -143,6 +145,9 @@ struct RowsParams {
     int splits;                 // parts of the channels, one cluster per tile
     int stages_a, stages_b, ring, smem, tmem_cols, d_cols;
 };
+// Up to this many rows the product runs without tensor memory and hand-offs (dq_rows_direct.cu)
+constexpr int kRowsDirect = 16;
+cudaError_t launch_rows_direct(const RowsParams& p, cudaStream_t st);
 void rows_plan(RowsParams& p);
 cudaError_t launch_rows(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const CUtensorMap& tm_x,
                         const CUtensorMap& tm_l2, const CUtensorMap& tm_u, const RowsParams& p, cudaStream_t st);
