@@ -89,7 +89,9 @@ def rows_reference(w: Weight, v: torch.Tensor, gelu: bool):
     if w.bias is not None:
         y = y + w.bias.double()
         A = A + w.bias.double().abs()
-    tol = 2 * U * (w.Ci / 16 + 32) * A + (2 * U * (w.Ci / 16 + 2 * w.rank + 32) + 2.0 ** -16) * B
+    a16 = v.abs().reshape(v.shape[0], -1, 16).amax(2).repeat_interleave(16, 1)
+    digits = 2.0 ** -17 * a16 + 2.0 ** -34 * v.abs().amax(1, keepdim=True)
+    tol = digits @ w_t(wv.abs()) + 2 * U * (w.Ci / 16 + 32) * A + (2 * U * (w.Ci / 16 + 2 * w.rank + 32) + 2.0 ** -16) * B
     if gelu:
         tol = 1.13 * tol + 3e-7 * y.abs().clamp(min=1.0)
         y = y * 0.5 * torch.special.erfc(-y / np.sqrt(2.0))

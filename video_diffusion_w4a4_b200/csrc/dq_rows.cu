@@ -37,16 +37,6 @@ namespace {
 
 // ------------------------------------------------------------------ PTX used by this file alone
 
-__device__ __forceinline__ float ld_dsmem_f32(uint32_t cluster_addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ void st_dsmem_f32(uint32_t cluster_addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
-}
-
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                            uint32_t accumulate) {
     asm volatile(
@@ -235,38 +225,6 @@ constexpr uint32_t kScaleBytes = 4 * 512;
 constexpr uint32_t kStageA = kCodeBytes + kScaleBytes;
 constexpr int kMaxStages = 16;
 constexpr int kMaxSmem = 225 * 1024;             // dynamic shared memory of a CTA that has an SM to itself
-
-// A place in a ring and the parity of its use, stepped without a division (a division by a runtime
-// ring size costs more than a chunk's MMAs)
-struct Ring {
-    int slot = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next(int size) {
-        if (++slot == size) {
-            slot = 0;
-            phase ^= 1;
-        }
-    }
-};
-
-// One lane's wait for the whole warp
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
-                                          uint64_t budget_ns) {
-    bool ok = true;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait_spin(bar, parity, abort_flag, status, budget_ns);
-    return __shfl_sync(0xffffffffu, ok, 0);
-}
-
-// One lane of a converged warp, the same every time
-__device__ __forceinline__ bool elect_one() {
-    uint32_t pred;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(pred));
-    return pred != 0;
-}
 
 struct MainBars {
     uint64_t fullA[kMaxStages], emptyA[kMaxStages], fullB[kMaxStages], emptyB[kMaxStages], tfull[8], tempty[8], accf;

@@ -7,6 +7,10 @@
 
 namespace dq {
 
+constexpr uint32_t kRowsCodeBytes = 128 * 128;   // codes of 128 output channels x 256 input channels
+constexpr uint32_t kRowsScaleBytes = 4 * 512;    // their group scales
+constexpr int kRowsStages = 16;                  // stages of an operand ring at most
+
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -147,6 +151,48 @@ __device__ __forceinline__ void store_lowrank(float* dst, int rank, int g, int t
         w0[0] = acc[n][0], w0[1] = acc[n][1];
         w0[8 * rank] = acc[n][2], w0[8 * rank + 1] = acc[n][3];
     }
+}
+
+// A place in a ring and the parity of its use, stepped without a division (a division by a runtime
+// ring size costs more than a chunk's MMAs)
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int size) {
+        if (++slot == size) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// One lane's wait for the whole warp
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                          uint64_t budget_ns) {
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait_spin(bar, parity, abort_flag, status, budget_ns);
+    return __shfl_sync(0xffffffffu, ok, 0);
+}
+
+// One lane of a converged warp, the same every time
+__device__ __forceinline__ bool elect_one() {
+    uint32_t pred;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(pred));
+    return pred != 0;
+}
+
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t cluster_addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_dsmem_f32(uint32_t cluster_addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 
 }  // namespace dq
