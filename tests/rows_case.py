@@ -6,6 +6,9 @@ Bounds (derived from the formulas; u = 2^-24, the fp32 rounding unit):
            absolute values A, the low-rank factor's intermediate kept as BF16 hi + lo (2^-16 of its
            terms B), then one rounding to BF16 (half a step, 2^-8 of the value).  GELU has a slope
            below 1.13 and an evaluation error of 3e-7 max(1, |y|).
+           The rows themselves enter as eight FP4 digits to the base 8: with the row's largest magnitude M
+           in [2^e, 2^(e+1)) a value has digits of 2^(e-1) 8^-p, p = 0..7, each rounded to nearest, so what
+           is left is at most 2^(e-1) 8^-7 / 2 = 2^(e-23) <= 2^-23 M.  Times the weights' magnitudes, summed.
   norm     a relative error of (C / 256 + 48) u: the sum of C squares in strides of at least 256
            threads and a tree, a division, a square root, a reciprocal and two products; then half a
            step of the format (BF16 2^-8, E4M3 2^-4 of the value, 2^-10 scales below its normal range).
@@ -89,8 +92,7 @@ def rows_reference(w: Weight, v: torch.Tensor, gelu: bool):
     if w.bias is not None:
         y = y + w.bias.double()
         A = A + w.bias.double().abs()
-    a16 = v.abs().reshape(v.shape[0], -1, 16).amax(2).repeat_interleave(16, 1)
-    digits = 2.0 ** -17 * a16 + 2.0 ** -34 * v.abs().amax(1, keepdim=True)
+    digits = 2.0 ** -23 * v.abs().amax(1, keepdim=True).expand_as(v)
     tol = digits @ w_t(wv.abs()) + 2 * U * (w.Ci / 16 + 32) * A + (2 * U * (w.Ci / 16 + 2 * w.rank + 32) + 2.0 ** -16) * B
     if gelu:
         tol = 1.13 * tol + 3e-7 * y.abs().clamp(min=1.0)

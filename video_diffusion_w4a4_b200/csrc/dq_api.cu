@@ -925,7 +925,6 @@ int dq_rows_forward(const void* X, int x_format, long long x_stride, const float
         p.u_part = (float*)(ws + wl.off_part);
         p.u_parts = dq::imin(dq::kRowsParts, Ci / 64);
         p.xh = (uint16_t*)(ws + wl.off_digits);
-        p.x_sf = ws + wl.off_sf;
         dq::rows_fp4_plan(p);
         if (!map_2d(&tm_x, p.xh, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Ci / 2, (uint64_t)rows * dq::kRowsDigits, 128, p.n_pad))
             return map_fail("digits");

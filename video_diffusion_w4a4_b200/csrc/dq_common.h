@@ -229,15 +229,15 @@ DQ_HD WsLayout ws_layout(const Geom& g, int Ci, int Co, int rank, int kgroup = 0
 }
 
 // Workspace of dq_rows_forward: the status word, the rows' factors (fp32), then
-//   few rows   partial sums of U = X L1 (kRowsParts x rows x rank fp32), the rows' digits (rows x 6 x
-//              Ci/2 bytes) and the digits' scales (1024 bytes per 64 channels and pass)
+//   few rows   partial sums of U = X L1 (kRowsParts x rows x rank fp32) and the rows' digits (rows x 8 x
+//              Ci/2 bytes)
 //   more rows  U as BF16 hi + lo (rows x slab) and the rows as FP16 (rows x 2 Ci: a scale per 64
 //              channels keeps hi and lo halves)
 // A workspace holds either, so that its size grows with the rows alone.
 constexpr int kRowsParts = 16;
 
 struct RowsLayout {
-    size_t total, off_status, off_e, off_u, off_xh, off_part, off_digits, off_sf;
+    size_t total, off_status, off_e, off_u, off_xh, off_part, off_digits;
 };
 
 DQ_HD RowsLayout rows_layout(int rows, int Ci, int rank) {
@@ -249,8 +249,7 @@ DQ_HD RowsLayout rows_layout(int rows, int Ci, int rank) {
     L.off_u = a;         a = align_up(a + (size_t)rows * slab_width(rank) * 2, kAlign);
     L.off_xh = a;        a = align_up(a + (size_t)rows * Ci * 4, kAlign);
     L.off_part = b;      b = align_up(b + (size_t)kRowsParts * rows * rank * 4, kAlign);
-    L.off_digits = b;    b = align_up(b + (size_t)rows * 3 * Ci, kAlign);
-    L.off_sf = b;        b = align_up(b + (size_t)cdiv(rows, 20) * (Ci / 64) * 1024, kAlign);
+    L.off_digits = b;    b = align_up(b + (size_t)rows * 4 * Ci, kAlign);
     L.total = a > b ? a : b;
     return L;
 }

@@ -138,8 +138,6 @@ struct RowsParams {
     uint16_t* u;                // rows x slab BF16: X L1 / (e S_W) as hi + lo
     float* u_part;              // up to kRowsDirect rows: u_parts x rows x rank partial sums of X L1
     int u_parts;
-    uint8_t* x_sf;              // FP4 form: the digits' scales (xh holds their codes)
-    int sf_groups;              //   128-column groups of scales per pass and 64-channel block
     int hilo;                   // xh holds hi and lo halves (a scale per 64 channels)
     uint64_t budget_ns;
     // the cut of the product (rows_plan)
@@ -150,9 +148,9 @@ struct RowsParams {
 // Up to this many rows the product runs without tensor memory and hand-offs (dq_rows_direct.cu)
 constexpr int kRowsDirect = 16;
 // Rows of X in FP4 digits (dq_rows_fp4.cu): digits per value, rows per pass
-constexpr int kRowsDigits = 6;
-constexpr int kRowsPass = 40;
-constexpr int kRowsFp4 = 80;
+constexpr int kRowsDigits = 8;
+constexpr int kRowsPass = 32;
+constexpr int kRowsFp4 = 64;
 void rows_fp4_plan(RowsParams& p);
 cudaError_t launch_rows_fp4(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const CUtensorMap& tm_x, const RowsParams& p,
                             cudaStream_t st);

@@ -3,27 +3,24 @@
 //
 // Few rows leave the weight's bytes as the bound, and decoding codes costs more
 // time than reading them.  Here they are not decoded: codes and group scales are
-// the A operand of kind::mxf4nvf4 as they lie in the packed weight, and the rows
-// of X are written exactly enough in the same format.  A group of 16 values with
-// largest magnitude in [2^e, 2^(e+1)) is a sum of kDigits = 6 FP4 digits,
-//   x = 2^(e-1) sum_p 8^-p d_p + r,   d_p in {-4, ..., 4},  |r| <= 2^(e-17),
-// d_p the nearest integer to what the digits before it leave.  A BF16 value at
-// least 2^-9 of its group's largest is exact, a smaller one off by at most 2^-17
-// of the largest; so are E4M3 codes (those are exact down to 2^-13), and code *
-// scale with a scale per 64 channels.  All digits of a group carry the scale
-// 2^(e-1) / E as E4M3 (2^-9 to 2^8, with E the row's power of two; a group below
-// 2^-17 of the row's largest is held relative to that), each digit is a column of
-// the MMA, and the epilogue sums a row's columns with their weights 8^-p in fp32.
+// the A operand of kind::mxf4nvf4 as they lie in the packed weight, and a row of X
+// is written in the same format as kDigits = 8 FP4 digits a value,
+//   x = 2^(e-1) sum_p 8^-p d_p + r,   d_p in {-4, ..., 4},  |r| <= 2^(e-23),
+// with 2^e <= max |x| < 2^(e+1) over the row and d_p the nearest integer to what
+// the digits before it leave: 24 bits of the row's largest value, what an fp32 sum
+// over the row keeps of it.  Each digit is a column of the MMA (the B scales are 1)
+// and the epilogue sums a row's columns with their weights 8^-p in fp32.
 //
-//   k_rows_digits   per row: digits, scales, E; beside it U = xv L1 in up to 16
+//   k_rows_digits   digits and 2^(e-1) per row; beside it U = xv L1 in up to 16
 //                   partial sums over the channels (mma.sync)
-//   k_rows_fp4      128 output channels (the MMA's M) times up to 40 rows (240
+//   k_rows_fp4      128 output channels (the MMA's M) times up to 32 rows (256
 //                   columns) per CTA.  One warp keeps codes and scales in flight,
-//                   one the digits, one lane issues scale copies and MMAs; when
-//                   the tiles alone do not fill the GPU a cluster splits the
-//                   channels and sums its parts in rank order through distributed
-//                   shared memory.  Its loads of the weight do not wait for
-//                   k_rows_digits (programmatic launch).
+//                   one the digits, one issues scale copies and MMAs, eight form
+//                   U L2 meanwhile and then the output.  When the tiles alone do
+//                   not fill the GPU a cluster splits the channels and sums its
+//                   parts in rank order through distributed shared memory.  The
+//                   loads of the weight do not wait for k_rows_digits
+//                   (programmatic launch).
 #include "../../include/deltaquant.h"
 #include "dq_common.h"
 #include "dq_internal.h"
@@ -40,50 +37,40 @@ constexpr int kDigits = kRowsDigits;
 
 constexpr int kPrepThreads = 256;
 
-// The values of 16 consecutive channels (group grp) of row m
+// The values of eight consecutive channels from c on of row m
 template <int kFmt>
-__device__ __forceinline__ void load_values16(const RowsParams& p, int m, int grp, float (&v)[16]) {
-    const long long off = (long long)m * p.x_stride + grp * 16;
+__device__ __forceinline__ void load_values8(const RowsParams& p, int m, int c, float (&v)[8]) {
+    const long long off = (long long)m * p.x_stride + c;
     if (kFmt == DQ_ROWS_BF16) {
-        const uint4* src = reinterpret_cast<const uint4*>((const uint16_t*)p.x + off);
-        const uint4 a = src[0], b = src[1];
-        const uint32_t r[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[2 * i] = bf16_lo(r[i]), v[2 * i + 1] = bf16_hi(r[i]);
-    } else {
-        const uint4 a = *reinterpret_cast<const uint4*>((const uint8_t*)p.x + off);
+        const uint4 a = *reinterpret_cast<const uint4*>((const uint16_t*)p.x + off);
         const uint32_t r[4] = {a.x, a.y, a.z, a.w};
-        const float s = kFmt == DQ_ROWS_E4M3_GROUP64 ? p.x_scales[(long long)m * (p.Ci / 64) + grp / 4] : 1.f;
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
+        for (int i = 0; i < 4; i++) v[2 * i] = bf16_lo(r[i]), v[2 * i + 1] = bf16_hi(r[i]);
+    } else {
+        const uint2 a = *reinterpret_cast<const uint2*>((const uint8_t*)p.x + off);
+        const uint32_t r[2] = {a.x, a.y};
+        const float s = kFmt == DQ_ROWS_E4M3_GROUP64 ? p.x_scales[(long long)m * (p.Ci / 64) + c / 64] : 1.f;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
             f16x2_values(e4m3x2_to_f16x2(r[i / 2] >> (16 * (i & 1))), v[2 * i], v[2 * i + 1]);
             if (kFmt == DQ_ROWS_E4M3_GROUP64) v[2 * i] *= s, v[2 * i + 1] *= s;
         }
     }
 }
 
-__device__ __forceinline__ float amax16(const float (&v)[16]) {
-    float a = fabsf(v[0]);
-#pragma unroll
-    for (int i = 1; i < 16; i++) a = max_nan(a, fabsf(v[i]));
-    return a;
-}
-
-// floor(log2 a), -126 for subnormals and zero
-__device__ __forceinline__ int exponent_of(float a) {
-    const int e = (int)((__float_as_uint(a) >> 23) & 255);
-    return e ? e - 127 : -126;
-}
-
+// Digits of the channels 2048 part to 2048 part + 2047 of row m (each CTA of a row finds the row's
+// largest magnitude for itself: a second read of at most 28 KB, from L2, instead of a hand-off).
 template <int kFmt>
-__device__ __forceinline__ void digits_of_row(const RowsParams& p, int m) {
+__device__ __forceinline__ void digits_of_row(const RowsParams& p, int m, int part) {
     __shared__ float sh[kPrepThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, groups = p.Ci / 16;
-    float v[16], am = 0.f;
-    for (int g = tid; g < groups; g += kPrepThreads) {
-        load_values16<kFmt>(p, m, g, v);
-        am = max_nan(am, amax16(v));
+    const int tid = threadIdx.x, lane = tid & 31, c = (part * kPrepThreads + tid) * 8;
+    float v[8], am = 0.f;
+    for (int i = tid * 8; i < p.Ci; i += kPrepThreads * 8) {
+        load_values8<kFmt>(p, m, i, v);
+#pragma unroll
+        for (int e = 0; e < 8; e++) am = max_nan(am, fabsf(v[e]));
     }
+    if (c < p.Ci) load_values8<kFmt>(p, m, c, v);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
     if (lane == 0) sh[tid >> 5] = am;
@@ -92,59 +79,40 @@ __device__ __forceinline__ void digits_of_row(const RowsParams& p, int m) {
 #pragma unroll
     for (int w = 1; w < kPrepThreads / 32; w++) am = max_nan(am, sh[w]);
     const bool finite = am < __int_as_float(0x7F800000);
-    const int K = exponent_of(am) - 9;              // E = 2^K; the largest group's scale is 2^8
-    if (tid == 0) {
-        float E = K >= -126 ? pow2i(K) : __int_as_float(1 << (K + 149));
+    const int eb = (int)((__float_as_uint(am) >> 23) & 255);
+    const int k = (eb ? eb - 127 : -126) - 1;       // the first digit's unit 2^k; |x 2^-k| < 4
+    if (part == 0 && tid == 0) {
+        float E = k >= -126 ? pow2i(k) : __int_as_float(1 << (k + 149));
         if (kFmt == DQ_ROWS_E4M3) E *= p.x_scales[m];
         p.e[m] = finite ? E : __int_as_float(0x7FC00000);   // a NaN or an infinity: NaN all over the row
     }
-    const int pass = m / p.n_rows, n0 = (m - pass * p.n_rows) * kDigits;   // the row's first column of its pass
-    uint8_t* codes = (uint8_t*)p.xh + (size_t)m * kDigits * (p.Ci / 2);
-    uint8_t* scales = p.x_sf + (size_t)pass * (p.Ci / 64) * p.sf_groups * 512;
-    // groups is a multiple of 16, so the four groups of a 64-channel block are in four lanes of one warp
-    for (int g = tid; g < groups; g += kPrepThreads) {
-        load_values16<kFmt>(p, m, g, v);
-        const float a = amax16(v);
-        int j = exponent_of(a) - 1 - K;             // scale 2^j, j <= 8
-        j = j < -9 ? -9 : j;
-        const uint32_t code = j >= -6 ? (uint32_t)(j + 7) << 3 : 4u >> (-7 - j);
-        const int k = -(K + j), h = k / 2;          // |value 2^k| < 4; k in [-126, 136]: two exact steps
-        const float f0 = pow2i(h), f1 = pow2i(k - h);
+    if (c >= p.Ci) return;
+    const int h = -k / 2;                            // two exact steps (k in [-127, 126])
+    const float f0 = pow2i(h), f1 = pow2i(-k - h);
 #pragma unroll
-        for (int i = 0; i < 16; i++) v[i] = finite ? v[i] * f0 * f1 : 0.f;
-        uint8_t* dst = codes + g * 8;
+    for (int i = 0; i < 8; i++) v[i] = finite ? v[i] * f0 * f1 : 0.f;
+    uint8_t* dst = (uint8_t*)p.xh + (size_t)m * kDigits * (p.Ci / 2) + c / 2;
 #pragma unroll
-        for (int q = 0; q < kDigits; q++) {
-            float d[16];
+    for (int q = 0; q < kDigits; q++) {
+        float d[8];
 #pragma unroll
-            for (int i = 0; i < 16; i++) {
-                d[i] = __fsub_rn(__fadd_rn(v[i], 12582912.f), 12582912.f);   // nearest integer
-                v[i] = (v[i] - d[i]) * 8.f;
-            }
-            *reinterpret_cast<uint2*>(dst + (size_t)q * (p.Ci / 2)) =
-                make_uint2(cvt_e2m1x8(*reinterpret_cast<const float(*)[8]>(&d[0])),
-                           cvt_e2m1x8(*reinterpret_cast<const float(*)[8]>(&d[8])));
+        for (int i = 0; i < 8; i++) {
+            d[i] = __fsub_rn(__fadd_rn(v[i], 12582912.f), 12582912.f);   // nearest integer
+            v[i] = (v[i] - d[i]) * 8.f;
         }
-        // one 32-bit word of scales per column and 64-channel block, the same for all of the row's columns
-        const unsigned mask = groups - (g - lane) >= 32 ? 0xffffffffu : 0xffffu;
-        uint32_t word = code << (8 * (lane & 3));
-        word |= __shfl_xor_sync(mask, word, 1);
-        word |= __shfl_xor_sync(mask, word, 2);
-        for (int q = lane & 3; q < kDigits; q += 4) {
-            const int n = n0 + q;
-            *reinterpret_cast<uint32_t*>(scales + ((size_t)(g >> 2) * p.sf_groups + (n >> 7)) * 512 + (n & 31) * 16 +
-                                         ((n & 127) >> 5) * 4) = word;
-        }
+        *reinterpret_cast<uint32_t*>(dst + (size_t)q * (p.Ci / 2)) = cvt_e2m1x8(d);
     }
 }
 
 template <int kNT, int kFmt>
 __global__ void __launch_bounds__(kPrepThreads) k_rows_digits(RowsParams p) {
     extern __shared__ float low_sm[];   // [8 warps][16][rank]
+    griddep_wait();     // the launch before this one may still read the workspace, or write X
     griddep_launch();
-    if ((int)blockIdx.x < p.rows) return digits_of_row<kFmt>(p, (int)blockIdx.x);
+    const int parts = (p.Ci + 2047) / 2048, block = (int)blockIdx.x;
+    if (block < p.rows * parts) return digits_of_row<kFmt>(p, block / parts, block % parts);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int part = ((int)blockIdx.x - p.rows) % p.u_parts, m0 = ((int)blockIdx.x - p.rows) / p.u_parts * 16;
+    const int part = (block - p.rows * parts) % p.u_parts, m0 = (block - p.rows * parts) / p.u_parts * 16;
     const int nm = imin(16, p.rows - m0), nblk = p.Ci / 64;
     const int b0 = nblk * part / p.u_parts, b1 = nblk * (part + 1) / p.u_parts;
     if (part == 0 && m0 == 0 && tid == 0) *p.status = header_ok(p) ? 0 : kStatusBadWeight;
@@ -173,19 +141,13 @@ __global__ void __launch_bounds__(kPrepThreads) k_rows_digits(RowsParams p) {
 
 constexpr int kMainThreads = 384;               // producers of A and B, MMA, a spare warp, eight epilogue warps
 constexpr int kEpiThreads = 256;
-constexpr int kMaxSmem = 225 * 1024;
+constexpr int kMaxSmem = 225 * 1024, kSmallSmem = 225 * 512;   // dynamic shared memory, one CTA or two per SM
 
 struct Fp4Bars {
-    uint64_t fullA[kRowsStages], fullB[kRowsStages], empty[kRowsStages], accf;
+    uint64_t full[kRowsStages], empty[kRowsStages], accf;
     uint32_t tmem;
     int abort_flag;
 };
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
 
 // 32 lanes x 16 bytes from shared memory to four columns of every 32-lane quadrant
 __device__ __forceinline__ void tmem_cp_32x128b(uint32_t taddr, uint64_t sdesc) {
@@ -210,9 +172,11 @@ __global__ void __launch_bounds__(kMainThreads, 2)
     __shared__ Fp4Bars bars;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int S = p.stages_a;
-    const uint32_t b_bytes = (uint32_t)p.n_pad * 128u, sf_bytes = (uint32_t)p.sf_groups * 2048u;
-    const uint32_t stage = kRowsCodeBytes + b_bytes + kRowsScaleBytes + sf_bytes;   // codes, digits, scales of both
-    float* su = (float*)(sm + (size_t)S * stage);                     // [rows of the pass][rank]
+    const uint32_t b_bytes = (uint32_t)p.n_pad * 128u;
+    const uint32_t stage = kRowsCodeBytes + b_bytes + kRowsScaleBytes;   // codes, digits, the codes' scales
+    float* su = (float*)(sm + (size_t)S * stage);                     // [rows of the pass][rank]: U
+    float* se = su + p.n_rows * p.rank;                               // [rows of the pass]: the rows' factors
+    float* slow = se + 64;                                            // [rows this CTA finishes][128]: U L2 + b
     volatile int* abort_flag = &bars.abort_flag;
     const int split = (int)blockIdx.x, splits = (int)gridDim.x;       // the cluster spans a tile's splits
     const int o0 = (int)blockIdx.y * 128;
@@ -222,8 +186,7 @@ __global__ void __launch_bounds__(kMainThreads, 2)
 
     if (tid == 0) {
         for (int s = 0; s < S; s++) {
-            mbar_init(&bars.fullA[s], 1);
-            mbar_init(&bars.fullB[s], 1);
+            mbar_init(&bars.full[s], 2);    // both producers
             mbar_init(&bars.empty[s], 1);
         }
         mbar_init(&bars.accf, 1);
@@ -234,10 +197,16 @@ __global__ void __launch_bounds__(kMainThreads, 2)
         tmem_alloc(&bars.tmem, (uint32_t)p.tmem_cols);
         tmem_relinquish();
     }
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&tm_w);
+        prefetch_tmap(&tm_s);
+    }
+    if (warp == 2 && lane == 0) prefetch_tmap(&tm_x);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = bars.tmem;
+    const uint32_t tmem = bars.tmem, t_one = tmem + (uint32_t)p.d_cols, t_sf = t_one + 8;
+    griddep_launch();
 
     if (warp == 0) {
         // ------------------------------------------------ codes and their scales
@@ -246,7 +215,7 @@ __global__ void __launch_bounds__(kMainThreads, 2)
             Ring r;
             int g = 0;
             for (; g < nA; g++, r.next(S)) {
-                uint64_t* full = &bars.fullA[r.slot];
+                uint64_t* full = &bars.full[r.slot];
                 if (g >= S && !mbar_wait(&bars.empty[r.slot], r.phase ^ 1, abort_flag, p.status, p.budget_ns)) break;
                 uint8_t* dst = sm + (size_t)r.slot * stage;
                 mbar_arrive_expect_tx(full, kRowsCodeBytes + kRowsScaleBytes);
@@ -255,64 +224,50 @@ __global__ void __launch_bounds__(kMainThreads, 2)
                 tma_load_4d(dst + kRowsCodeBytes + b_bytes, &tm_s, full, 0, half, 0, blk0 + 4 * g);
             }
             for (int q = g > S ? g - S : 0; q < g; q++)   // every copy lands before shared memory is released
-                mbar_wait(&bars.fullA[q % S], (uint32_t)(q / S) & 1, abort_flag, nullptr, p.budget_ns, false);
+                mbar_wait(&bars.full[q % S], (uint32_t)(q / S) & 1, abort_flag, nullptr, p.budget_ns, false);
         }
         __syncwarp();
     } else if (warp == 2) {
-        // ------------------------------------------------ digits and their scales
+        // ------------------------------------------------ digits
         if (lane == 0) {
             griddep_wait();
-            const uint8_t* sf = p.x_sf + ((size_t)blockIdx.z * (p.Ci / 64) + a0 * 4) * p.sf_groups * 512;
             Ring r;
             int g = 0;
             for (; g < nA; g++, r.next(S)) {
-                uint64_t* full = &bars.fullB[r.slot];
+                uint64_t* full = &bars.full[r.slot];
                 if (g >= S && !mbar_wait(&bars.empty[r.slot], r.phase ^ 1, abort_flag, p.status, p.budget_ns)) break;
-                uint8_t* dst = sm + (size_t)r.slot * stage + kRowsCodeBytes;
-                mbar_arrive_expect_tx(full, b_bytes + sf_bytes);
-                tma_load_2d(dst, &tm_x, full, (a0 + g) * 128, m0 * kDigits);
-                bulk_load(dst + b_bytes + kRowsScaleBytes, sf + (size_t)g * sf_bytes, sf_bytes, full);
+                mbar_arrive_expect_tx(full, b_bytes);
+                tma_load_2d(sm + (size_t)r.slot * stage + kRowsCodeBytes, &tm_x, full, (a0 + g) * 128, m0 * kDigits);
             }
             for (int q = g > S ? g - S : 0; q < g; q++)
-                mbar_wait(&bars.fullB[q % S], (uint32_t)(q / S) & 1, abort_flag, nullptr, p.budget_ns, false);
+                mbar_wait(&bars.full[q % S], (uint32_t)(q / S) & 1, abort_flag, nullptr, p.budget_ns, false);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ MMAs (one elected lane; the warp's control flow is uniform)
         const uint32_t idesc = idesc_nvfp4(128, p.n_pad);
-        const bool wide = p.sf_groups == 2;                       // more than 128 columns: eight scale columns a block
-        const uint32_t sf_cols = wide ? 48 : 32;                  // a stage's scale columns: 16 of A, 16 or 32 of B
         const uint32_t base = smem_u32(sm);
+        bar_sync(2, 32 + 128);   // the digits' scales are in tensor memory
+        tc_fence_after();
         Ring r;
-        for (int g = 0; g < nA; g++, r.next(S)) {
-            if (!warp_wait(&bars.fullA[r.slot], r.phase, abort_flag, p.status, p.budget_ns)) break;
-            if (!warp_wait(&bars.fullB[r.slot], r.phase, abort_flag, p.status, p.budget_ns)) break;
+        uint32_t sa = base, ta = t_sf;
+        for (int g = 0; g < nA; g++) {
+            if (!__all_sync(0xffffffffu, mbar_wait_spin(&bars.full[r.slot], r.phase, abort_flag, p.status, p.budget_ns))) break;
             tc_fence_after();
-            const uint32_t sa = base + (uint32_t)r.slot * stage;
-            const uint64_t ad = desc_k_sw128(sa), bd = desc_k_sw128(sa + kRowsCodeBytes);
-            const uint64_t fa = smem_desc(sa + kRowsCodeBytes + b_bytes, 128, 128, 0);
-            const uint64_t fb = fa + (kRowsScaleBytes >> 4);
-            const uint32_t ta = tmem + (uint32_t)p.d_cols + (uint32_t)r.slot * sf_cols, tb = ta + 16;
             if (elect_one()) {
+                const uint64_t ad = desc_k_sw128(sa), bd = desc_k_sw128(sa + kRowsCodeBytes);
+                const uint64_t fa = smem_desc(sa + kRowsCodeBytes + b_bytes, 128, 128, 0);
                 // the stage's own columns: nothing still reads them, as its empty barrier was waited for
 #pragma unroll
                 for (int j = 0; j < 4; j++) tmem_cp_32x128b(ta + 4 * j, fa + 32 * j);
-                if (!wide) {
 #pragma unroll
-                    for (int j = 0; j < 4; j++) tmem_cp_32x128b(tb + 4 * j, fb + 32 * j);
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        mma_nvfp4(tmem, ad + 2 * j, bd + 2 * j, idesc, ta + 4 * j, tb + 4 * j, (g | j) != 0);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; j++) tmem_cp_32x128b(tb + 4 * j, fb + 32 * j);
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        mma_nvfp4(tmem, ad + 2 * j, bd + 2 * j, idesc, ta + 4 * j, tb + 8 * j, (g | j) != 0);
-                }
+                for (int j = 0; j < 4; j++) mma_nvfp4(tmem, ad + 2 * j, bd + 2 * j, idesc, ta + 4 * j, t_one, (g | j) != 0);
                 tc_commit(&bars.empty[r.slot]);
             }
             __syncwarp();
+            sa += stage, ta += 16;
+            r.next(S);
+            if (r.slot == 0) sa = base, ta = t_sf;
         }
         if (elect_one()) {
             tc_commit(&bars.accf);
@@ -325,70 +280,85 @@ __global__ void __launch_bounds__(kMainThreads, 2)
     const int quad = warp & 3, group = (warp - 4) >> 2, row = quad * 32 + lane, et = tid - 128;
     const PackedHeader* hdr = reinterpret_cast<const PackedHeader*>(p.packed_w);
     const float S_W = hdr->S_W;
-    const int r2 = p.rank / 2;
+    // the rows of the pass that this CTA finishes: every splits-th
+    const int mine = split < nm ? (nm - split + splits - 1) / splits : 0;
     bool done = true, ok = true;
-    float bv = 0.f;
     if (warp >= 4) {
+        if (warp < 8) {
+            // the digits' scales: E4M3 1 in eight columns of every lane
+            const uint32_t one = 0x38383838u, at = t_one + ((uint32_t)(quad * 32) << 16);
+            tmem_st_x4(at, one, one, one, one);
+            tmem_st_x4(at + 4, one, one, one, one);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            asm volatile("bar.arrive 2, 160;" ::: "memory");
+        }
         ok = header_ok(p);
+        float bv = 0.f;
         if (hdr->flags & kPackedHasBias) bv = *(const float*)(p.packed_w + p.off_bias + 4ll * (o0 + row));
-        griddep_wait();   // the rows' factors and U come from k_rows_digits
+        // U, the rows' factors and U L2 + b while the weight streams in
+        griddep_wait();
         for (int e = et; e < nm * p.rank; e += kEpiThreads) {
             float s = 0.f;
             for (int c = 0; c < p.u_parts; c++) s += p.u_part[((long long)c * p.rows + m0) * p.rank + e];
             if (p.x_format == DQ_ROWS_E4M3) s *= p.x_scales[m0 + e / p.rank];
             su[e] = s;
         }
+        if (et < nm) se[et] = p.e[m0 + et];
+        bar_sync(1, kEpiThreads);
+        const uint4* l2 = reinterpret_cast<const uint4*>(p.l2 + (size_t)(o0 + row) * p.slab);
+        for (int i0 = 4 * group; i0 < mine; i0 += 8) {
+            float low[4] = {bv, bv, bv, bv};
+            for (int j = 0; j < p.rank; j += 8) {
+                const uint4 w = l2[j / 8];
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    if (i0 + i < mine) {
+                        const float4* u = reinterpret_cast<const float4*>(su + (split + (i0 + i) * splits) * p.rank + j);
+                        const float4 u0 = u[0], u1 = u[1];
+                        low[i] = fmaf(u0.x, bf16_lo(ww[0]), low[i]);
+                        low[i] = fmaf(u0.y, bf16_hi(ww[0]), low[i]);
+                        low[i] = fmaf(u0.z, bf16_lo(ww[1]), low[i]);
+                        low[i] = fmaf(u0.w, bf16_hi(ww[1]), low[i]);
+                        low[i] = fmaf(u1.x, bf16_lo(ww[2]), low[i]);
+                        low[i] = fmaf(u1.y, bf16_hi(ww[2]), low[i]);
+                        low[i] = fmaf(u1.z, bf16_lo(ww[3]), low[i]);
+                        low[i] = fmaf(u1.w, bf16_hi(ww[3]), low[i]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                if (i0 + i < mine) slow[(i0 + i) * 128 + row] = low[i];
+        }
         bar_sync(1, kEpiThreads);
         if (lane == 0) done = mbar_wait(&bars.accf, 0, abort_flag, p.status, p.budget_ns);
         done = __shfl_sync(0xffffffffu, done, 0);
         tc_fence_after();
     }
-    const uint32_t* l2 = reinterpret_cast<const uint32_t*>(p.l2 + (size_t)(o0 + row) * p.slab);
-    // Y of this thread's output channel for the rows m + i * step (i < cnt <= 8) with main sums v
-    auto finish = [&](int m, int step, int cnt, const float (&v)[8]) {
-        float low[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++) low[i] = 0.f;
-        for (int j = 0; j < r2; j += 4) {
-            const uint4 w = *reinterpret_cast<const uint4*>(l2 + j);
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                if (i < cnt) {
-                    const float4* u = reinterpret_cast<const float4*>(su + (m + i * step) * p.rank + 2 * j);
-                    const float4 u0 = u[0], u1 = u[1];
-                    low[i] = fmaf(u0.x, bf16_lo(ww[0]), low[i]);
-                    low[i] = fmaf(u0.y, bf16_hi(ww[0]), low[i]);
-                    low[i] = fmaf(u0.z, bf16_lo(ww[1]), low[i]);
-                    low[i] = fmaf(u0.w, bf16_hi(ww[1]), low[i]);
-                    low[i] = fmaf(u1.x, bf16_lo(ww[2]), low[i]);
-                    low[i] = fmaf(u1.y, bf16_hi(ww[2]), low[i]);
-                    low[i] = fmaf(u1.z, bf16_lo(ww[3]), low[i]);
-                    low[i] = fmaf(u1.w, bf16_hi(ww[3]), low[i]);
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            if (i >= cnt) break;
-            const bool two = i + 1 < cnt;
-            float y0 = fmaf(v[i] * S_W, p.e[m0 + m + i * step], low[i] + bv);
-            float y1 = two ? fmaf(v[i + 1] * S_W, p.e[m0 + m + (i + 1) * step], low[i + 1] + bv) : 0.f;
-            if (p.gelu) f2_unpack(gelu_erf2(f2_pack(y0, y1)), y0, y1);
-            uint16_t* dst = p.y + (long long)(m0 + m + i * step) * p.y_stride + o0 + row;
-            dst[0] = f32_to_bf16_rn(y0);
-            if (two) dst[(long long)step * p.y_stride] = f32_to_bf16_rn(y1);
-        }
+    // Y of this thread's output channel for the rows i, i + 1 of those this CTA finishes (the second where
+    // it exists), from their main sums
+    auto finish = [&](int i, float v0, float v1) {
+        const bool two = i + 1 < mine;
+        const int m = split + i * splits;
+        float y0 = fmaf(v0 * S_W, se[m], slow[i * 128 + row]);
+        float y1 = two ? fmaf(v1 * S_W, se[m + splits], slow[(i + 1) * 128 + row]) : 0.f;
+        if (p.gelu) f2_unpack(gelu_erf2(f2_pack(y0, y1)), y0, y1);
+        uint16_t* dst = p.y + (long long)(m0 + m) * p.y_stride + o0 + row;
+        dst[0] = f32_to_bf16_rn(y0);
+        if (two) dst[(long long)splits * p.y_stride] = f32_to_bf16_rn(y1);
     };
-    // main sums of the rows 8 b to 8 b + 7: their digits' columns with weights 8^-p
-    auto columns = [&](int b, float (&v)[8]) {
-        uint32_t acc[48];
+    // main sums of the rows 4 b to 4 b + 3: their digits' columns with weights 8^-p
+    auto columns = [&](int b, float (&v)[4]) {
+        uint32_t acc[32];
 #pragma unroll
-        for (int c = 0; c < 48; c += 16)
-            tmem_ld_x16(tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(48 * b + c), *reinterpret_cast<uint32_t(*)[16]>(&acc[c]));
+        for (int c = 0; c < 32; c += 16)
+            tmem_ld_x16(tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(32 * b + c), *reinterpret_cast<uint32_t(*)[16]>(&acc[c]));
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
+        for (int i = 0; i < 4; i++) {
             v[i] = __uint_as_float(acc[kDigits * i + kDigits - 1]);
 #pragma unroll
             for (int q = kDigits - 2; q >= 0; q--) v[i] = fmaf(v[i], 0.125f, __uint_as_float(acc[kDigits * i + q]));
@@ -396,10 +366,11 @@ __global__ void __launch_bounds__(kMainThreads, 2)
     };
     if (splits == 1) {
         if (warp >= 4 && done && ok) {
-            for (int b = group; 8 * b < nm; b += 2) {
-                float v[8];
+            for (int b = group; 4 * b < nm; b += 2) {
+                float v[4];
                 columns(b, v);
-                finish(8 * b, 1, imin(8, nm - 8 * b), v);
+                finish(4 * b, v[0], v[1]);
+                if (4 * b + 2 < nm) finish(4 * b + 2, v[2], v[3]);
             }
         }
     } else {
@@ -410,13 +381,13 @@ __global__ void __launch_bounds__(kMainThreads, 2)
         float* red = (float*)sm;   // [source CTA][row / splits][128 output channels]
         const int own = (nm + splits - 1) / splits;
         if (warp >= 4 && done) {
-            for (int b = group; 8 * b < nm; b += 2) {
-                float v[8];
+            for (int b = group; 4 * b < nm; b += 2) {
+                float v[4];
                 columns(b, v);
-                int dst = (8 * b) % splits, at = (8 * b) / splits;
+                int dst = (4 * b) % splits, at = (4 * b) / splits;
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    if (8 * b + i < nm)
+                for (int i = 0; i < 4; i++) {
+                    if (4 * b + i < nm)
                         st_dsmem_f32(mapa_shared(smem_u32(&red[(split * own + at) * 128 + row]), (uint32_t)dst), v[i]);
                     if (++dst == splits) dst = 0, at++;
                 }
@@ -425,16 +396,13 @@ __global__ void __launch_bounds__(kMainThreads, 2)
         __syncwarp();
         cluster_sync();
         if (warp >= 4 && done && ok) {
-            const int mine = split < nm ? (nm - split + splits - 1) / splits : 0;   // rows split, split + splits, ...
-            for (int i0 = 8 * group; i0 < mine; i0 += 16) {
-                float v[8];
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    v[i] = 0.f;
-                    if (i0 + i < mine)
-                        for (int q = 0; q < splits; q++) v[i] += red[(q * own + i0 + i) * 128 + row];
+            for (int i = 2 * group; i < mine; i += 4) {
+                float v0 = 0.f, v1 = 0.f;
+                for (int q = 0; q < splits; q++) {
+                    v0 += red[(q * own + i) * 128 + row];
+                    if (i + 1 < mine) v1 += red[(q * own + i + 1) * 128 + row];
                 }
-                finish(split + i0 * splits, splits, imin(8, mine - i0), v);
+                finish(i, v0, v1);
             }
         }
     }
@@ -449,14 +417,22 @@ __global__ void __launch_bounds__(kMainThreads, 2)
 template <int kNT>
 cudaError_t launch_digits(const RowsParams& p, cudaStream_t st) {
     const size_t smem = (size_t)(kPrepThreads / 32) * 16 * p.rank * 4;
-    const unsigned grid = (unsigned)(p.rows + p.u_parts * cdiv(p.rows, 16));
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(p.rows * cdiv(p.Ci, 2048) + p.u_parts * cdiv(p.rows, 16)));
+    cfg.blockDim = dim3(kPrepThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     auto go = [&](auto kernel) {
         if (smem > 48 * 1024) {
             cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             if (e != cudaSuccess) return e;
         }
-        kernel<<<grid, kPrepThreads, smem, st>>>(p);
-        return cudaGetLastError();
+        return cudaLaunchKernelEx(&cfg, kernel, p);
     };
     if (p.x_format == DQ_ROWS_BF16) return go(k_rows_digits<kNT, DQ_ROWS_BF16>);
     if (p.x_format == DQ_ROWS_E4M3) return go(k_rows_digits<kNT, DQ_ROWS_E4M3>);
@@ -470,24 +446,23 @@ void rows_fp4_plan(RowsParams& p) {
     const int passes = (int)cdiv(p.rows, kRowsPass);
     p.n_rows = (int)cdiv(p.rows, passes);
     p.passes = (int)cdiv(p.rows, p.n_rows);
-    p.n_pad = (int)cdiv(p.n_rows * kDigits, 8) * 8;
-    p.sf_groups = p.n_pad > 128 ? 2 : 1;
+    p.n_pad = p.n_rows * kDigits;
     // Up to 16 rows two CTAs share an SM (256 tensor-memory columns and at most 113 KB each).  Each
     // takes more than a third of the SM's shared memory, so that a third CTA never waits there for
     // tensor memory while its cluster waits for it.
     const bool small = p.n_rows <= 16;
-    p.d_cols = (int)cdiv(p.n_rows, 8) * 48;
+    p.d_cols = (int)cdiv(p.n_pad, 32) * 32;
     p.tmem_cols = small ? 256 : 512;
-    const int stage = (int)(kRowsCodeBytes + kRowsScaleBytes) + p.n_pad * 128 + p.sf_groups * 2048;
-    const int extra = p.n_rows * p.rank * 4 + 1024, room = (small ? 111 * 1024 : kMaxSmem) - extra;
-    const int by_tmem = (p.tmem_cols - p.d_cols) / (p.sf_groups == 2 ? 48 : 32);
-    p.stages_a = imin(imin(kRowsStages, room / stage), by_tmem);
-    p.smem = p.stages_a * stage + extra;
-    if (p.smem < 80 * 1024) p.smem = 80 * 1024;
+    const int stage = (int)(kRowsCodeBytes + kRowsScaleBytes) + p.n_pad * 128;
     // as many parts of the channels as still let every CTA be resident at once
     const int tiles = p.Co / 128 * p.passes, places = small ? 296 : 148;
     p.splits = 1;
     while (p.splits < 8 && tiles * p.splits * 2 <= places && p.splits * 2 <= p.Ci / 256) p.splits *= 2;
+    const int extra = (p.n_rows * p.rank + 64 + (int)cdiv(p.n_rows, p.splits) * 128) * 4 + 1024;
+    const int room = (small ? kSmallSmem : kMaxSmem) - extra;
+    p.stages_a = imin(imin(kRowsStages, room / stage), (p.tmem_cols - p.d_cols - 8) / 16);
+    p.smem = p.stages_a * stage + extra;
+    if (p.smem < 80 * 1024) p.smem = 80 * 1024;
 }
 
 cudaError_t launch_rows_fp4(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const CUtensorMap& tm_x, const RowsParams& p,
