@@ -438,19 +438,23 @@ def dq_linear_forward_noalloc(X, T, H, W, t, h, w, Ci, Co, rank, packed_W, L1_mm
 
 # ------------------------------------------------------------------ few rows (device)
 
-def _same_device(fn: str, *tensors) -> None:
-    """The library launches on the current CUDA device: refuse torch tensors that live elsewhere."""
-    dev = None
+def _device_ptrs(fn: str, *tensors) -> list:
+    """Device addresses of torch tensors (raw integers and None as they are).  The library launches on the
+    current CUDA device: tensors that live elsewhere are refused."""
+    out, cur = [], None
     for x in tensors:
-        if x is None or isinstance(x, int) or not hasattr(x, "get_device"):
+        if x is None or x.__class__ is int:
+            out.append(x)
             continue
-        d = x.get_device()
-        if dev is None:
+        dev = x.get_device()
+        if dev != cur:
             import torch
-            dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
-        if d != dev:
-            where = "in host memory" if d < 0 else f"on device {d}"
-            raise ValueError(f"{fn}: a tensor is {where}, the current CUDA device is {dev}")
+            if cur is not None or dev < 0 or dev != torch.cuda.current_device():
+                raise ValueError(f"{fn}: a tensor is {'in host memory' if dev < 0 else f'on device {dev}'}, not on the "
+                                 "current CUDA device")
+            cur = dev
+        out.append(x.data_ptr())
+    return out
 
 
 def dq_rmsnorm_forward(X, rows: int, C: int, Y, x_stride: int = 0, residual=None, residual_stride: int = 0,
@@ -458,10 +462,9 @@ def dq_rmsnorm_forward(X, rows: int, C: int, Y, x_stride: int = 0, residual=None
                        y_stride: int = 0, y_scales=None, stream=None) -> None:
     """Y = RMS norm of X + residual, in BF16 or E4M3 with scales; sum_out = BF16(X + residual).
     Strides in elements, 0 for contiguous rows (include/deltaquant.h)."""
-    _same_device("dq_rmsnorm_forward", X, residual, sum_out, gamma, Y, y_scales)
-    rc = _lib.dq_rmsnorm_forward(_ptr(X), x_stride, _ptr(residual), residual_stride, _ptr(gamma), rows, C, eps,
-                                 _ptr(sum_out), sum_stride, y_format, _ptr(Y), y_stride, _ptr(y_scales),
-                                 _stream(stream))
+    x, r, so, g, y, sc = _device_ptrs("dq_rmsnorm_forward", X, residual, sum_out, gamma, Y, y_scales)
+    rc = _lib.dq_rmsnorm_forward(x, x_stride, r, residual_stride, g, rows, C, eps, so, sum_stride, y_format, y, y_stride,
+                                 sc, stream if stream is None else _stream(stream))
     _check("dq_rmsnorm_forward", rc)
 
 
@@ -476,10 +479,9 @@ def dq_rows_forward(X, rows: int, Ci: int, Co: int, rank: int, packed_W, L1_mma,
                     epilogue: int = DQ_EPILOGUE_NONE, y_stride: int = 0, stream=None) -> None:
     """Y = the packed layer applied to few rows that are not quantised further: BF16, or E4M3 codes
     with scales (x_format, x_scales).  Strides in elements, 0 for contiguous rows (include/deltaquant.h)."""
-    _same_device("dq_rows_forward", X, x_scales, packed_W, L1_mma, L2_slab, Y, workspace)
-    rc = _lib.dq_rows_forward(_ptr(X), x_format, x_stride, _ptr(x_scales), rows, Ci, Co, rank, _ptr(packed_W),
-                              _ptr(L1_mma), _ptr(L2_slab), epilogue, _ptr(Y), y_stride, _ptr(workspace),
-                              workspace_bytes, _stream(stream))
+    x, sc, w, l1, l2, y, ws = _device_ptrs("dq_rows_forward", X, x_scales, packed_W, L1_mma, L2_slab, Y, workspace)
+    rc = _lib.dq_rows_forward(x, x_format, x_stride, sc, rows, Ci, Co, rank, w, l1, l2, epilogue, y, y_stride, ws,
+                              workspace_bytes, stream if stream is None else _stream(stream))
     _check("dq_rows_forward", rc)
 
 

@@ -27,6 +27,8 @@
 #include "dq_ptx.cuh"
 #include "dq_rows.cuh"
 
+#include <atomic>
+
 namespace dq {
 
 namespace {
@@ -414,6 +416,28 @@ __global__ void __launch_bounds__(kMainThreads, 2)
     }
 }
 
+// Runs `set` (a kernel's attributes) on the first call for that kernel on the current device.  Concurrent
+// first calls may both run it; they set the same values.
+template <typename Set>
+cudaError_t once_per_device(const void* kernel, Set set) {
+    constexpr int kKernels = 16, kDevices = 64;
+    static std::atomic<const void*> names[kKernels];
+    static std::atomic<uint64_t> done[kKernels];   // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int i = 0;
+    for (; i < kKernels; i++) {
+        const void* at = names[i].load(std::memory_order_acquire);
+        if (at == nullptr && !names[i].compare_exchange_strong(at, kernel)) at = names[i].load(std::memory_order_acquire);
+        if (at == nullptr || at == kernel) break;
+    }
+    if (i == kKernels || dev >= kDevices) return set();
+    if (done[i].load(std::memory_order_acquire) >> dev & 1) return cudaSuccess;
+    if ((e = set()) == cudaSuccess) done[i].fetch_or(1ull << dev, std::memory_order_release);
+    return e;
+}
+
 template <int kNT>
 cudaError_t launch_digits(const RowsParams& p, cudaStream_t st) {
     const size_t smem = (size_t)(kPrepThreads / 32) * 16 * p.rank * 4;
@@ -428,10 +452,14 @@ cudaError_t launch_digits(const RowsParams& p, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     auto go = [&](auto kernel) {
-        if (smem > 48 * 1024) {
-            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return e;
-        }
+        // the product's split of the SM between L1 and shared memory: a different one would keep its CTAs
+        // off an SM until this kernel's have left
+        const cudaError_t e = once_per_device((const void*)kernel, [&] {
+            cudaError_t e1 = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                  (kPrepThreads / 32) * 16 * 8 * kNT * 4);
+            return e1 != cudaSuccess ? e1 : cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        });
+        if (e != cudaSuccess) return e;
         return cudaLaunchKernelEx(&cfg, kernel, p);
     };
     if (p.x_format == DQ_ROWS_BF16) return go(k_rows_digits<kNT, DQ_ROWS_BF16>);
@@ -472,7 +500,10 @@ cudaError_t launch_rows_fp4(const CUtensorMap& tm_w, const CUtensorMap& tm_s, co
                     : p.rank <= 64 ? launch_digits<8>(p, st)
                                    : launch_digits<16>(p, st);
     if (e != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(k_rows_fp4, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem)) != cudaSuccess) return e;
+    e = once_per_device((const void*)k_rows_fp4, [] {
+        return cudaFuncSetAttribute(k_rows_fp4, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    });
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
