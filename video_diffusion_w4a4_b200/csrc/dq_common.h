@@ -228,16 +228,11 @@ DQ_HD WsLayout ws_layout(const Geom& g, int Ci, int Co, int rank, int kgroup = 0
     return L;
 }
 
-// Workspace of dq_rows_forward: the status word, the rows' factors (fp32), then
-//   few rows   partial sums of U = X L1 (kRowsParts x rows x rank fp32) and the rows' digits (rows x 8 x
-//              Ci/2 bytes)
-//   more rows  U as BF16 hi + lo (rows x slab) and the rows as FP16 (rows x 2 Ci: a scale per 64
-//              channels keeps hi and lo halves)
-// A workspace holds either, so that its size grows with the rows alone.
-constexpr int kRowsParts = 16;
-
+// Workspace of dq_rows_forward: the status word, the rows' factors (fp32), U as BF16 hi + lo (rows x
+// slab) and the product's B operand, four bytes a value: eight FP4 digits, or FP16 (hi and lo halves
+// with a scale per 64 channels).
 struct RowsLayout {
-    size_t total, off_status, off_e, off_u, off_xh, off_part, off_digits;
+    size_t total, off_status, off_e, off_u, off_xh;
 };
 
 DQ_HD RowsLayout rows_layout(int rows, int Ci, int rank) {
@@ -245,12 +240,9 @@ DQ_HD RowsLayout rows_layout(int rows, int Ci, int rank) {
     size_t off = 0;
     L.off_status = off;  off = align_up(off + 16, kAlign);
     L.off_e = off;       off = align_up(off + (size_t)rows * 4, kAlign);
-    size_t a = off, b = off;
-    L.off_u = a;         a = align_up(a + (size_t)rows * slab_width(rank) * 2, kAlign);
-    L.off_xh = a;        a = align_up(a + (size_t)rows * Ci * 4, kAlign);
-    L.off_part = b;      b = align_up(b + (size_t)kRowsParts * rows * rank * 4, kAlign);
-    L.off_digits = b;    b = align_up(b + (size_t)rows * 4 * Ci, kAlign);
-    L.total = a > b ? a : b;
+    L.off_u = off;       off = align_up(off + (size_t)rows * slab_width(rank) * 2, kAlign);
+    L.off_xh = off;      off = align_up(off + (size_t)rows * Ci * 4, kAlign);
+    L.total = off;
     return L;
 }
 

@@ -135,9 +135,7 @@ struct RowsParams {
     int* status;
     float* e;                   // rows: factor of each row of xh
     uint16_t* xh;               // rows x Ci FP16 (rows x 2 Ci with hilo): the product's B operand
-    uint16_t* u;                // rows x slab BF16: X L1 / (e S_W) as hi + lo
-    float* u_part;              // up to kRowsDirect rows: u_parts x rows x rank partial sums of X L1
-    int u_parts;
+    uint16_t* u;                // rows x slab BF16: X L1 as hi + lo (over e S_W for the FP16 product)
     int hilo;                   // xh holds hi and lo halves (a scale per 64 channels)
     uint64_t budget_ns;
     // the cut of the product (rows_plan)
@@ -145,16 +143,14 @@ struct RowsParams {
     int splits;                 // parts of the channels, one cluster per tile
     int stages_a, stages_b, ring, smem, tmem_cols, d_cols;
 };
-// Up to this many rows the product runs without tensor memory and hand-offs (dq_rows_direct.cu)
-constexpr int kRowsDirect = 16;
 // Rows of X in FP4 digits (dq_rows_fp4.cu): digits per value, rows per pass
 constexpr int kRowsDigits = 8;
 constexpr int kRowsPass = 32;
 constexpr int kRowsFp4 = 64;
 void rows_fp4_plan(RowsParams& p);
-cudaError_t launch_rows_fp4(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const CUtensorMap& tm_x, const RowsParams& p,
-                            cudaStream_t st);
-cudaError_t launch_rows_direct(const RowsParams& p, cudaStream_t st);
+cudaError_t launch_rows_fp4(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const CUtensorMap& tm_x, const CUtensorMap& tm_l2,
+                            const CUtensorMap& tm_u, const RowsParams& p, cudaStream_t st);
+cudaError_t launch_rows_prepare(const RowsParams& p, bool digit_form, cudaStream_t st);
 void rows_plan(RowsParams& p);
 cudaError_t launch_rows(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const CUtensorMap& tm_x,
                         const CUtensorMap& tm_l2, const CUtensorMap& tm_u, const RowsParams& p, cudaStream_t st);

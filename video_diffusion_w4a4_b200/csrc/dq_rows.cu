@@ -61,173 +61,31 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[
         : "memory");
 }
 
-// ------------------------------------------------------------------ rows -> B operand and U
-
-constexpr int kPrepThreads = 256, kPrepWarps = 8, kPrepCluster = 8, kPrepRows = 16;
-
-// x 2^-k in two exact steps (k in [-140, 113])
-struct Scale2 {
-    float a, b;
-};
-__device__ __forceinline__ Scale2 inv_scale(int k) {
-    const int h = (-k) / 2;
-    return Scale2{pow2i(h), pow2i(-k - h)};
-}
-
-template <int kNT, int kFmt>
-__global__ void __launch_bounds__(kPrepThreads) k_rows_prepare(RowsParams p) {
-    extern __shared__ float prep_sm[];
-    // [8 warps][16][rank] partial sums, then [16][rank] of this CTA, [8][16] maxima, [16] of this CTA
-    float* wpart = prep_sm;
-    float* part = wpart + kPrepWarps * kPrepRows * p.rank;
-    float* wmax = part + kPrepRows * p.rank;
-    float* cmax = wmax + kPrepWarps * kPrepRows;
-    int* rexp = (int*)(cmax + kPrepRows);       // [16] exponents k
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int crank = (int)cluster_ctarank();
-    const int m0 = (int)(blockIdx.x / kPrepCluster) * kPrepRows;
-    const int nm = imin(kPrepRows, p.rows - m0);
-    const int nblk = p.Ci / 64, b0 = nblk * crank / kPrepCluster, b1 = nblk * (crank + 1) / kPrepCluster;
-    griddep_launch();
-    if (blockIdx.x == 0 && tid == 0) *p.status = header_ok(p) ? 0 : kStatusBadWeight;
-    const float S_W = reinterpret_cast<const PackedHeader*>(p.packed_w)->S_W;
-
-    // X L1 of this CTA's channels: a warp takes 64 channels at a time, lane t of a quad 16 of them
-    float acc[kNT][4];
-#pragma unroll
-    for (int n = 0; n < kNT; n++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) acc[n][i] = 0.f;
-    float am0 = 0.f, am1 = 0.f;
-    for (int b = b0 + warp; b < b1; b += kPrepWarps) {
-        uint32_t xa[2][8];
-        float sc[2];
-        load_rows_16<kFmt>(p, m0, nm, b, g, t, xa, sc);
-        if (kFmt != DQ_ROWS_E4M3) {
-            float a[2] = {0.f, 0.f};
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-                    a[h] = max_nan(a[h], max_nan(fabsf(bf16_lo(xa[h][i])), fabsf(bf16_hi(xa[h][i]))));
-                if (kFmt == DQ_ROWS_E4M3_GROUP64) a[h] = fabsf(a[h] * sc[h]);
-            }
-            am0 = max_nan(am0, a[0]), am1 = max_nan(am1, a[1]);
-        }
-        lowrank_block<kNT, kFmt>(p, b, g, t, xa, sc, acc);
-    }
-    store_lowrank<kNT>(wpart + warp * kPrepRows * p.rank, p.rank, g, t, acc);
-    if (kFmt != DQ_ROWS_E4M3) {
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            am0 = max_nan(am0, __shfl_xor_sync(0xffffffffu, am0, o));
-            am1 = max_nan(am1, __shfl_xor_sync(0xffffffffu, am1, o));
-        }
-        if (t == 0) wmax[warp * kPrepRows + g] = am0, wmax[warp * kPrepRows + g + 8] = am1;
-    }
-    __syncthreads();
-    for (int e = tid; e < kPrepRows * p.rank; e += kPrepThreads) {
-        float s = 0.f;
-        for (int w = 0; w < kPrepWarps; w++) s += wpart[w * kPrepRows * p.rank + e];
-        part[e] = s;
-    }
-    if (kFmt != DQ_ROWS_E4M3 && tid < kPrepRows) {
-        float a = 0.f;
-        for (int w = 0; w < kPrepWarps; w++) a = max_nan(a, wmax[w * kPrepRows + tid]);
-        cmax[tid] = a;
-    }
-    cluster_sync();
-    // the row's factor E: the product's epilogue multiplies by it
-    if (tid < kPrepRows) {
-        int k = 0;
-        float E = 1.f;
-        if (kFmt == DQ_ROWS_E4M3) {
-            E = tid < nm ? p.x_scales[m0 + tid] : 0.f;
-        } else {
-            float a = 0.f;
-            for (int c = 0; c < kPrepCluster; c++) a = max_nan(a, ld_dsmem_f32(mapa_shared(smem_u32(&cmax[tid]), c)));
-            if (!(a < __int_as_float(0x7F800000))) {
-                E = __int_as_float(0x7FC00000);   // a NaN or an infinity in the row: NaN all over it
-            } else if (a > 0.f) {
-                k = row_exponent(a);
-                E = k >= -126 ? pow2i(k) : __int_as_float(1 << (k + 149));
-            }
-        }
-        rexp[tid] = k;
-        if (crank == 0 && tid < nm) p.e[m0 + tid] = E;
-    }
-    __syncthreads();
-    // U / (E S_W) as BF16 hi + lo, an eighth of the (row, rank) pairs per CTA; zeros up to the slab's width
-    for (int e = tid + crank * kPrepThreads; e < nm * p.rank; e += kPrepThreads * kPrepCluster) {
-        const int m = e / p.rank, j = e - m * p.rank;
-        const uint32_t at = smem_u32(&part[e]);
-        float u = 0.f;
-        for (int c = 0; c < kPrepCluster; c++) u += ld_dsmem_f32(mapa_shared(at, c));
-        const Scale2 s = inv_scale(rexp[m]);
-        u = u / S_W * s.a * s.b;
-        const float hi = bf16_lo(bf16x2_rn(u, 0.f));
-        uint16_t* dst = p.u + (long long)(m0 + m) * p.slab;
-        dst[j] = f32_to_bf16_rn(hi);
-        dst[p.rank + j] = f32_to_bf16_rn(u - hi);
-        for (int z = 2 * p.rank + j; z < p.slab; z += p.rank) dst[z] = 0;
-    }
-    // this CTA's channels as FP16
-    const int nv = (b1 - b0) * 8, ld = p.hilo ? 2 * p.Ci : p.Ci;
-    for (int i = tid; i < nm * nv; i += kPrepThreads) {
-        const int m = i / nv, c = b0 * 64 + (i - m * nv) * 8;
-        const long long off = (long long)(m0 + m) * p.x_stride + c;
-        uint16_t* dst = p.xh + (long long)(m0 + m) * ld + c;
-        uint32_t w[4];
-        if (kFmt == DQ_ROWS_E4M3) {
-            const uint2 q = *reinterpret_cast<const uint2*>((const uint8_t*)p.x + off);
-            w[0] = e4m3x2_to_f16x2(q.x), w[1] = e4m3x2_to_f16x2(q.x >> 16);
-            w[2] = e4m3x2_to_f16x2(q.y), w[3] = e4m3x2_to_f16x2(q.y >> 16);
-            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-            const Scale2 s = inv_scale(rexp[m]);
-            float v[8];
-            if (kFmt == DQ_ROWS_BF16) {
-                const uint4 q = *reinterpret_cast<const uint4*>((const uint16_t*)p.x + off);
-                const uint32_t r[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int j = 0; j < 4; j++) v[2 * j] = bf16_lo(r[j]), v[2 * j + 1] = bf16_hi(r[j]);
-            } else {
-                const uint2 q = *reinterpret_cast<const uint2*>((const uint8_t*)p.x + off);
-                const float gs = p.x_scales[(long long)(m0 + m) * nblk + c / 64];
-                const uint32_t r[2] = {q.x, q.y};
-#pragma unroll
-                for (int j = 0; j < 8; j++) v[j] = e4m3_to_f32(r[j / 4] >> (8 * (j & 3))) * gs;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; j++) v[j] = v[j] * s.a * s.b;
-#pragma unroll
-            for (int j = 0; j < 4; j++) w[j] = f16x2_rn(v[2 * j], v[2 * j + 1]);
-            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-            if (kFmt == DQ_ROWS_E4M3_GROUP64) {
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    float f0, f1;
-                    f16x2_values(w[j], f0, f1);
-                    w[j] = f16x2_rn(v[2 * j] - f0, v[2 * j + 1] - f1);
-                }
-                *reinterpret_cast<uint4*>(dst + p.Ci) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
-    }
-    cluster_sync();   // no CTA leaves while another still reads its sums
+// Eight E2M1 codes (value 2i in the low nibble of byte i) times the FP16 pair s -> four FP16 pairs
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t s, uint32_t* out) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        ".reg .b32 t0, t1, t2, t3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 t0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 t1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 t2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 t3, b3;\n\t"
+        "mul.rn.f16x2 %0, t0, %5;\n\t"
+        "mul.rn.f16x2 %1, t1, %5;\n\t"
+        "mul.rn.f16x2 %2, t2, %5;\n\t"
+        "mul.rn.f16x2 %3, t3, %5;\n\t}"
+        : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3])
+        : "r"(w), "r"(s));
 }
 
 // ------------------------------------------------------------------ the product
 
 constexpr int kMainThreads = 384;               // producers (A, B), MMA, a spare warp, eight decoding warps
-constexpr uint32_t kCodeBytes = 128 * 128;      // 128 output channels x 256 input channels
-constexpr uint32_t kScaleBytes = 4 * 512;
-constexpr uint32_t kStageA = kCodeBytes + kScaleBytes;
-constexpr int kMaxStages = 16;
+constexpr uint32_t kRowsStageA = kRowsCodeBytes + kRowsScaleBytes;   // 128 output x 256 input channels
 constexpr int kMaxSmem = 225 * 1024;             // dynamic shared memory of a CTA that has an SM to itself
 
 struct MainBars {
-    uint64_t fullA[kMaxStages], emptyA[kMaxStages], fullB[kMaxStages], emptyB[kMaxStages], tfull[8], tempty[8], accf;
+    uint64_t fullA[kRowsStages], emptyA[kRowsStages], fullB[kRowsStages], emptyB[kRowsStages], tfull[8], tempty[8], accf;
     uint32_t tmem;
     int abort_flag;
 };
@@ -242,7 +100,7 @@ __global__ void __launch_bounds__(kMainThreads, 2)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int SA = p.stages_a, SB = p.stages_b, R = p.ring;
     const uint32_t slotB = (uint32_t)p.n_pad * 128u;
-    uint8_t* ringB = sm + (size_t)SA * kStageA;
+    uint8_t* ringB = sm + (size_t)SA * kRowsStageA;
     volatile int* abort_flag = &bars.abort_flag;
     const int split = (int)blockIdx.x, splits = (int)gridDim.x;       // the cluster spans a tile's splits
     const int o0 = (int)blockIdx.y * 128;
@@ -287,14 +145,14 @@ __global__ void __launch_bounds__(kMainThreads, 2)
             for (; g < total; g++, r.next(SA)) {
                 uint64_t* full = &bars.fullA[r.slot];
                 if (g >= SA && !mbar_wait(&bars.emptyA[r.slot], r.phase ^ 1, abort_flag, p.status, p.budget_ns)) break;
-                uint8_t* dst = sm + (size_t)r.slot * kStageA;
+                uint8_t* dst = sm + (size_t)r.slot * kRowsStageA;
                 if (g < nA) {
-                    mbar_arrive_expect_tx(full, kStageA);
+                    mbar_arrive_expect_tx(full, kRowsStageA);
                     tma_load_2d(dst, &tm_w, full, (a0 + g) * 128, o0);
                     // 32 lanes x 16 bytes per 64-channel block: one half of the 256-row tile
-                    tma_load_4d(dst + kCodeBytes, &tm_s, full, 0, half, 0, blk0 + 4 * g);
+                    tma_load_4d(dst + kRowsCodeBytes, &tm_s, full, 0, half, 0, blk0 + 4 * g);
                 } else {
-                    mbar_arrive_expect_tx(full, kCodeBytes);
+                    mbar_arrive_expect_tx(full, kRowsCodeBytes);
                     tma_load_2d(dst, &tm_l2, full, (g - nA) * 64, o0);
                 }
             }
@@ -334,10 +192,10 @@ __global__ void __launch_bounds__(kMainThreads, 2)
         Ring rt, rb;
         bool alive = true;
         for (int c = 0; alive && c < chunks; c++, rt.next(R)) {
-            if (!(alive = warp_wait(&bars.tfull[rt.slot], rt.phase, abort_flag, p.status, p.budget_ns))) break;
+            if (!(alive = __all_sync(0xffffffffu, mbar_wait_spin(&bars.tfull[rt.slot], rt.phase, abort_flag, p.status, p.budget_ns)))) break;
             const uint32_t at = ring0 + (uint32_t)(32 * rt.slot);
             for (int h = 0; h < tiles; h++, rb.next(SB)) {
-                if (!(alive = warp_wait(&bars.fullB[rb.slot], rb.phase, abort_flag, p.status, p.budget_ns))) break;
+                if (!(alive = __all_sync(0xffffffffu, mbar_wait_spin(&bars.fullB[rb.slot], rb.phase, abort_flag, p.status, p.budget_ns)))) break;
                 tc_fence_after();
                 const uint64_t bd = bdesc0 + (uint64_t)((uint32_t)rb.slot * (slotB >> 4));
                 if (elect_one()) {
@@ -356,7 +214,7 @@ __global__ void __launch_bounds__(kMainThreads, 2)
             if (!warp_wait(&bars.fullA[sa], (uint32_t)(ga / SA) & 1, abort_flag, p.status, p.budget_ns)) break;
             if (!warp_wait(&bars.fullB[rb.slot], rb.phase, abort_flag, p.status, p.budget_ns)) break;
             tc_fence_after();
-            const uint64_t ad = desc_k_sw128(smem_u32(sm + (size_t)sa * kStageA));
+            const uint64_t ad = desc_k_sw128(smem_u32(sm + (size_t)sa * kRowsStageA));
             const uint64_t bd = bdesc0 + (uint64_t)((uint32_t)rb.slot * (slotB >> 4));
             if (elect_one()) {
 #pragma unroll
@@ -381,11 +239,11 @@ __global__ void __launch_bounds__(kMainThreads, 2)
         rt.slot = group;   // the ring's size is even: a group keeps to its places
         for (int c = group; c < chunks; c += 2) {
             if (!warp_wait(&bars.fullA[ra.slot], ra.phase, abort_flag, p.status, p.budget_ns)) break;
-            const uint8_t* st = sm + (size_t)ra.slot * kStageA;
+            const uint8_t* st = sm + (size_t)ra.slot * kRowsStageA;
             const uint32_t j0 = 2 * (c & 3);
             const uint4 w0 = *reinterpret_cast<const uint4*>(st + at + ((j0 ^ x16) << 4));
             const uint4 w1 = *reinterpret_cast<const uint4*>(st + at + (((j0 + 1) ^ x16) << 4));
-            const uint32_t sw = *reinterpret_cast<const uint32_t*>(st + kCodeBytes + (c & 3) * 512 + lane * 16 + quad * 4);
+            const uint32_t sw = *reinterpret_cast<const uint32_t*>(st + kRowsCodeBytes + (c & 3) * 512 + lane * 16 + quad * 4);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.emptyA[ra.slot]);
             const uint32_t s01 = e4m3x2_to_f16x2(sw), s23 = e4m3x2_to_f16x2(sw >> 16);
@@ -489,32 +347,6 @@ __global__ void __launch_bounds__(kMainThreads, 2)
     }
 }
 
-template <int kNT>
-cudaError_t launch_prepare(const RowsParams& p, cudaStream_t st) {
-    const size_t smem = ((size_t)(kPrepWarps + 1) * kPrepRows * p.rank + (kPrepWarps + 2) * kPrepRows) * 4;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kPrepCluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(cdiv(p.rows, kPrepRows) * kPrepCluster));
-    cfg.blockDim = dim3(kPrepThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    auto go = [&](auto kernel) {
-        if (smem > 48 * 1024) {
-            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return e;
-        }
-        return cudaLaunchKernelEx(&cfg, kernel, p);
-    };
-    if (p.x_format == DQ_ROWS_BF16) return go(k_rows_prepare<kNT, DQ_ROWS_BF16>);
-    if (p.x_format == DQ_ROWS_E4M3) return go(k_rows_prepare<kNT, DQ_ROWS_E4M3>);
-    return go(k_rows_prepare<kNT, DQ_ROWS_E4M3_GROUP64>);
-}
-
 }  // namespace
 
 // How the product of `rows` rows is cut (RowsParams' fields from n_rows on).
@@ -530,8 +362,8 @@ void rows_plan(RowsParams& p) {
     p.ring = small ? 6 : 8;
     const int slot = p.n_pad * 128, room = small ? 110 * 1024 : kMaxSmem - 1024;
     p.stages_b = small ? (p.n_pad <= 16 ? 8 : p.n_pad <= 32 ? 6 : 4) : (p.n_pad <= 128 ? 6 : 4);
-    p.stages_a = imin(kMaxStages, (room - p.stages_b * slot) / (int)kStageA);
-    p.smem = p.stages_a * (int)kStageA + p.stages_b * slot + 1024;
+    p.stages_a = imin(kRowsStages, (room - p.stages_b * slot) / (int)kRowsStageA);
+    p.smem = p.stages_a * (int)kRowsStageA + p.stages_b * slot + 1024;
     // as many parts of the channels as still let every CTA be resident at once
     const int tiles = p.Co / 128 * p.passes, places = small ? 296 : 148;
     p.splits = 1;
@@ -540,13 +372,12 @@ void rows_plan(RowsParams& p) {
 
 cudaError_t launch_rows(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const CUtensorMap& tm_x, const CUtensorMap& tm_l2,
                         const CUtensorMap& tm_u, const RowsParams& p, cudaStream_t st) {
-    cudaError_t e = p.rank <= 16   ? launch_prepare<2>(p, st)
-                    : p.rank <= 32 ? launch_prepare<4>(p, st)
-                    : p.rank <= 64 ? launch_prepare<8>(p, st)
-                                   : launch_prepare<16>(p, st);
+    cudaError_t e = launch_rows_prepare(p, false, st);
     if (e != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(k_rows_main, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem)) != cudaSuccess)
-        return e;
+    e = once_per_device((const void*)k_rows_main, [] {
+        return cudaFuncSetAttribute(k_rows_main, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    });
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
