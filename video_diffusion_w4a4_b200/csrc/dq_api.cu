@@ -923,12 +923,13 @@ int dq_rows_forward(const void* X, int x_format, long long x_stride, const float
     if (!map_sfb_lanes(&tm_s, p.packed_w + pl.off_scales, Ci, Co)) return map_fail("weight scales");
     if (!map_2d(&tm_l2, L2_slab, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pl.slab, Co, 64, 128)) return map_fail("L2");
     if (rows <= dq::kRowsFp4) {
-        dq::rows_fp4_plan(p);
+        cudaError_t e = dq::rows_fp4_plan(p);
+        if (e != cudaSuccess) return cuda_fail(e, "few-row product");
         if (!map_2d(&tm_x, p.xh, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Ci / 2, (uint64_t)rows * dq::kRowsDigits, 128, p.n_pad))
             return map_fail("digits");
         if (!map_2d(&tm_u, p.u, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pl.slab, rows, 64, (uint32_t)dq::cdiv(p.n_rows, 16) * 16))
             return map_fail("U");
-        cudaError_t e = dq::launch_rows_fp4(tm_w, tm_s, tm_x, tm_l2, tm_u, p, (cudaStream_t)stream);
+        e = dq::launch_rows_fp4(tm_w, tm_s, tm_x, tm_l2, tm_u, p, (cudaStream_t)stream);
         return e == cudaSuccess ? DQ_OK : cuda_fail(e, "few-row product");
     }
     dq::rows_plan(p);

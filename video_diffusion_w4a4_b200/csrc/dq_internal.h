@@ -142,12 +142,14 @@ struct RowsParams {
     int n_rows, n_pad, passes;  // rows of X per pass, that rounded up to 16
     int splits;                 // parts of the channels, one cluster per tile
     int stages_a, stages_b, ring, smem, tmem_cols, d_cols;
+    int own_digits;             // FP4 product: its CTAs write the digits of their channels themselves
 };
 // Rows of X in FP4 digits (dq_rows_fp4.cu): digits per value, rows per pass
 constexpr int kRowsDigits = 8;
 constexpr int kRowsPass = 32;
 constexpr int kRowsFp4 = 64;
-void rows_fp4_plan(RowsParams& p);
+constexpr int kRowsOwn = 8;   // rows whose digits the product's CTAs may write themselves
+cudaError_t rows_fp4_plan(RowsParams& p);
 cudaError_t launch_rows_fp4(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const CUtensorMap& tm_x, const CUtensorMap& tm_l2,
                             const CUtensorMap& tm_u, const RowsParams& p, cudaStream_t st);
 cudaError_t launch_rows_prepare(const RowsParams& p, bool digit_form, cudaStream_t st);

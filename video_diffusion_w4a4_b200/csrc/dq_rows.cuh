@@ -73,6 +73,48 @@ __device__ __forceinline__ uint32_t next_digits8(float (&v)[8]) {
     return cvt_e2m1x8(d);
 }
 
+// The values of eight consecutive channels from c on of row m
+template <int kFmt>
+__device__ __forceinline__ void load_values8(const RowsParams& p, int m, int c, float (&v)[8]) {
+    const long long off = (long long)m * p.x_stride + c;
+    if (kFmt == DQ_ROWS_BF16) {
+        const uint4 a = *reinterpret_cast<const uint4*>((const uint16_t*)p.x + off);
+        const uint32_t r[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[2 * i] = bf16_lo(r[i]), v[2 * i + 1] = bf16_hi(r[i]);
+    } else {
+        const uint2 a = *reinterpret_cast<const uint2*>((const uint8_t*)p.x + off);
+        const uint32_t r[2] = {a.x, a.y};
+        const float s = kFmt == DQ_ROWS_E4M3_GROUP64 ? p.x_scales[(long long)m * (p.Ci / 64) + c / 64] : 1.f;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            f16x2_values(e4m3x2_to_f16x2(r[i / 2] >> (16 * (i & 1))), v[2 * i], v[2 * i + 1]);
+            if (kFmt == DQ_ROWS_E4M3_GROUP64) v[2 * i] *= s, v[2 * i + 1] *= s;
+        }
+    }
+}
+
+// Exponent k of a row's power of two E = 2^k from its largest magnitude: the first digit's unit (values
+// below 4 units), or what moves the row to at most 2^15; subnormals count as 2^-126.  E4M3 codes need none in
+// the FP16 form.
+template <int kFmt, bool kDigitForm>
+__device__ __forceinline__ int row_unit(float am) {
+    if (!kDigitForm && kFmt == DQ_ROWS_E4M3) return 0;
+    const int e = (int)((__float_as_uint(am) >> 23) & 255);
+    return (e ? e - 127 : -126) - (kDigitForm ? 1 : 14);
+}
+
+__device__ __forceinline__ bool finite_row(float am) { return am < __int_as_float(0x7F800000); }
+
+// v 2^-k in two exact steps (k in [-140, 126])
+struct Scale2 {
+    float a, b;
+};
+__device__ __forceinline__ Scale2 inv_scale(int k) {
+    const int h = (-k) / 2;
+    return Scale2{pow2i(h), pow2i(-k - h)};
+}
+
 // A place in a ring and the parity of its use, stepped without a division (a division by a runtime
 // ring size costs more than a chunk's MMAs)
 struct Ring {

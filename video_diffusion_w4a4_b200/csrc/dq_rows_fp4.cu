@@ -40,8 +40,9 @@ constexpr int kEpiThreads = 256;
 constexpr int kMaxSmem = 225 * 1024, kSmallSmem = 225 * 512;   // dynamic shared memory, one CTA or two per SM
 
 struct Fp4Bars {
-    uint64_t full[kRowsStages], empty[kRowsStages], accf;
+    uint64_t full[kRowsStages], empty[kRowsStages], accf, digits;
     float e[kRowsPass];   // the rows' factors
+    float amax[8];        // own digits: each warp's part of its row's largest magnitude
     uint32_t tmem;
     int abort_flag;
 };
@@ -69,6 +70,56 @@ __device__ __forceinline__ void mma_nvfp4(uint32_t d_tmem, uint64_t adesc, uint6
         : "memory");
 }
 
+// Own digits (at most kRowsOwn rows): the epilogue warps, idle while the weight streams in, write the digits of
+// this CTA's channels into shared memory as the MMA reads them, with the power of two of the rows' values in these
+// channels alone.  Each row takes 8 / (rows rounded up to a power of two) warps.
+template <int kFmt>
+__device__ __forceinline__ void write_own_digits(const RowsParams& p, Fp4Bars& bars, uint8_t* dst, int c0, int channels) {
+    const int ew = (int)(threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
+    const int per = p.rows == 1 ? 8 : p.rows == 2 ? 4 : p.rows <= 4 ? 2 : 1, m = ew / per, part = ew % per;
+    float v[8], am = 0.f;
+    if (m < p.rows) {
+#pragma unroll 4
+        for (int c = (part * 32 + lane) * 8; c < channels; c += per * 256) {
+            load_values8<kFmt>(p, m, c0 + c, v);
+#pragma unroll
+            for (int i = 0; i < 8; i++) am = max_nan(am, fabsf(v[i]));
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
+    if (lane == 0) bars.amax[ew] = am;
+    bar_sync(1, kEpiThreads);
+    if (m < p.rows) {
+        for (int i = 0; i < per; i++) am = max_nan(am, bars.amax[m * per + i]);
+        const bool finite = finite_row(am);
+        const int k = row_unit<kFmt, true>(am);
+        if (part == 0 && lane == 0) {
+            float E = k >= -126 ? pow2i(k) : __int_as_float(1 << (k + 149));
+            if (kFmt == DQ_ROWS_E4M3) E *= p.x_scales[m];
+            bars.e[m] = finite ? E : __int_as_float(0x7FC00000);
+        }
+        const Scale2 s = inv_scale(k);
+#pragma unroll 2
+        for (int c = (part * 32 + lane) * 8; c < channels; c += per * 256) {
+            load_values8<kFmt>(p, m, c0 + c, v);
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] = finite ? v[i] * s.a * s.b : 0.f;
+            // column 8 m + q of the 256-channel stage c / 256: row 8 m + q of 128 bytes, its 16-byte pieces
+            // permuted by the row's low bits (128-byte swizzle)
+            uint8_t* row = dst + (size_t)(c >> 8) * p.n_pad * 128 + m * 1024 + ((c >> 1) & 15);
+            const int piece = (c >> 5) & 7;
+#pragma unroll
+            for (int q = 0; q < kDigits; q++)
+                *reinterpret_cast<uint32_t*>(row + q * 128 + ((piece ^ q) << 4)) = next_digits8(v);
+        }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the MMA reads them
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.digits);
+    bar_sync(1, kEpiThreads);   // the factors, for every epilogue warp
+}
+
 __global__ void __launch_bounds__(kMainThreads, 2)
     k_rows_fp4(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_s,
                const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_l2,
@@ -78,7 +129,8 @@ __global__ void __launch_bounds__(kMainThreads, 2)
     __shared__ Fp4Bars bars;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int S = p.stages_a;
-    const uint32_t b_bytes = (uint32_t)p.n_pad * 128u;
+    const bool own = p.own_digits != 0;
+    const uint32_t b_all = (uint32_t)p.n_pad * 128u, b_bytes = own ? 0u : b_all;   // digits of a stage; in the ring
     const uint32_t stage = kRowsCodeBytes + b_bytes + kRowsScaleBytes;   // codes, digits, the codes' scales
     volatile int* abort_flag = &bars.abort_flag;
     const int split = (int)blockIdx.x, splits = (int)gridDim.x;       // the cluster spans a tile's splits
@@ -88,13 +140,15 @@ __global__ void __launch_bounds__(kMainThreads, 2)
     const int k256 = p.Ci / 256, a0 = k256 * split / splits, nA = k256 * (split + 1) / splits - a0;
     const int total = nA + (split == 0 ? p.slab / 64 : 0);           // stages: the weight's, then the low-rank factor's
     const uint32_t n16 = (uint32_t)(p.n_rows + 15) & ~15u;
+    uint8_t* digits = sm + (size_t)S * stage;                         // own digits: [stage][column][128 bytes]
 
     if (tid == 0) {
         for (int s = 0; s < S; s++) {
-            mbar_init(&bars.full[s], 2);    // both producers
+            mbar_init(&bars.full[s], own ? 1 : 2);   // one producer, or both
             mbar_init(&bars.empty[s], 1);
         }
         mbar_init(&bars.accf, 1);
+        mbar_init(&bars.digits, kEpiThreads / 32);
         bars.abort_flag = 0;
         fence_barrier_init();
     }
@@ -128,9 +182,14 @@ __global__ void __launch_bounds__(kMainThreads, 2)
                     tma_load_2d(dst, &tm_w, full, (a0 + g) * 128, o0);
                     // 32 lanes x 16 bytes per 64-channel block: one half of the 256-row tile
                     tma_load_4d(dst + kRowsCodeBytes + b_bytes, &tm_s, full, 0, half, 0, blk0 + 4 * g);
-                } else {
+                } else if (!own) {
                     mbar_arrive_expect_tx(full, kRowsCodeBytes);
                     tma_load_2d(dst, &tm_l2, full, (g - nA) * 64, o0);
+                } else {
+                    if (g == nA) griddep_wait();   // U comes from k_rows_prepare
+                    mbar_arrive_expect_tx(full, kRowsCodeBytes + n16 * 128);
+                    tma_load_2d(dst, &tm_l2, full, (g - nA) * 64, o0);
+                    tma_load_2d(dst + kRowsCodeBytes, &tm_u, full, (g - nA) * 64, m0);
                 }
             }
             for (int q = g > S ? g - S : 0; q < g; q++)   // every copy lands before shared memory is released
@@ -139,7 +198,7 @@ __global__ void __launch_bounds__(kMainThreads, 2)
         __syncwarp();
     } else if (warp == 2) {
         // ------------------------------------------------ digits, then U
-        if (lane == 0) {
+        if (lane == 0 && !own) {
             griddep_wait();
             Ring r;
             int g = 0;
@@ -164,15 +223,19 @@ __global__ void __launch_bounds__(kMainThreads, 2)
         const uint32_t idesc = idesc_nvfp4(128, p.n_pad), id_low = idesc_bf16(128, (int)n16);
         const uint32_t base = smem_u32(sm);
         bar_sync(2, 32 + 128);   // the digits' scales are in tensor memory
+        bool alive = true;
+        if (own) alive = __all_sync(0xffffffffu, mbar_wait_spin(&bars.digits, 0, abort_flag, p.status, p.budget_ns));
         tc_fence_after();
         Ring r;
-        uint32_t sa = base, ta = t_sf;
-        for (int g = 0; g < total; g++) {
+        uint32_t sa = base, ta = t_sf, sb = own ? smem_u32(digits) : base + kRowsCodeBytes;
+        const uint32_t b_step = own ? b_all : stage;
+        for (int g = 0; alive && g < total; g++) {
             if (!__all_sync(0xffffffffu, mbar_wait_spin(&bars.full[r.slot], r.phase, abort_flag, p.status, p.budget_ns))) break;
             tc_fence_after();
             if (elect_one()) {
-                const uint64_t ad = desc_k_sw128(sa), bd = desc_k_sw128(sa + kRowsCodeBytes);
+                const uint64_t ad = desc_k_sw128(sa);
                 if (g < nA) {
+                    const uint64_t bd = desc_k_sw128(sb);
                     const uint64_t fa = smem_desc(sa + kRowsCodeBytes + b_bytes, 128, 128, 0);
                     // the stage's own columns: nothing still reads them, as its empty barrier was waited for
 #pragma unroll
@@ -182,14 +245,17 @@ __global__ void __launch_bounds__(kMainThreads, 2)
                         mma_nvfp4(tmem, ad + 2 * j, bd + 2 * j, idesc, ta + 4 * j, t_one, (g | j) != 0);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 4; j++) mma_bf16(t_low, ad + 2 * j, bd + 2 * j, id_low, (g > nA || j) ? 1u : 0u);
+                    for (int j = 0; j < 4; j++) mma_bf16(t_low, ad + 2 * j, desc_k_sw128(sa + kRowsCodeBytes) + 2 * j, id_low, (g > nA || j) ? 1u : 0u);
                 }
                 tc_commit(&bars.empty[r.slot]);
             }
             __syncwarp();
-            sa += stage, ta += 16;
+            sa += stage, ta += 16, sb += b_step;
             r.next(S);
-            if (r.slot == 0) sa = base, ta = t_sf;
+            if (r.slot == 0) {
+                sa = base, ta = t_sf;
+                if (!own) sb = base + kRowsCodeBytes;
+            }
         }
         if (elect_one()) {
             tc_commit(&bars.accf);
@@ -218,9 +284,19 @@ __global__ void __launch_bounds__(kMainThreads, 2)
         }
         ok = header_ok(p);
         if (hdr->flags & kPackedHasBias) bv = *(const float*)(p.packed_w + p.off_bias + 4ll * (o0 + row));
-        griddep_wait();   // the rows' factors come from k_rows_prepare
-        if (et < nm) bars.e[et] = p.e[m0 + et];
-        bar_sync(1, kEpiThreads);
+        if (own) {
+            uint8_t* dst = digits;
+            if (p.x_format == DQ_ROWS_BF16)
+                write_own_digits<DQ_ROWS_BF16>(p, bars, dst, a0 * 256, nA * 256);
+            else if (p.x_format == DQ_ROWS_E4M3)
+                write_own_digits<DQ_ROWS_E4M3>(p, bars, dst, a0 * 256, nA * 256);
+            else
+                write_own_digits<DQ_ROWS_E4M3_GROUP64>(p, bars, dst, a0 * 256, nA * 256);
+        } else {
+            griddep_wait();   // the rows' factors come from k_rows_prepare
+            if (et < nm) bars.e[et] = p.e[m0 + et];
+            bar_sync(1, kEpiThreads);
+        }
         if (lane == 0) done = mbar_wait(&bars.accf, 0, abort_flag, p.status, p.budget_ns);
         done = __shfl_sync(0xffffffffu, done, 0);
         tc_fence_after();
@@ -302,37 +378,85 @@ __global__ void __launch_bounds__(kMainThreads, 2)
 
 }  // namespace
 
+namespace {
+
+cudaError_t set_attributes() {
+    return once_per_device((const void*)k_rows_fp4, [] {
+        return cudaFuncSetAttribute(k_rows_fp4, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    });
+}
+
+// Clusters of `splits` CTAs that fit on the current device at once, asked once per device and configuration.
+cudaError_t resident_clusters(bool small, int splits, int* clusters) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][2][9];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= kDevices) return cudaErrorInvalidDevice;
+    std::atomic<int>& k = known[dev][small][splits];
+    if ((*clusters = k.load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    if ((e = set_attributes()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)splits, 1024);
+    cfg.blockDim = dim3(kMainThreads);
+    cfg.dynamicSmemBytes = small ? kSmallSmem : kMaxSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaOccupancyMaxActiveClusters(clusters, k_rows_fp4, &cfg)) != cudaSuccess) return e;
+    k.store(*clusters, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+}  // namespace
+
 // How the product of `rows` rows is cut (RowsParams' fields from n_rows on).
-void rows_fp4_plan(RowsParams& p) {
+cudaError_t rows_fp4_plan(RowsParams& p) {
     const int passes = (int)cdiv(p.rows, kRowsPass);
     p.n_rows = (int)cdiv(p.rows, passes);
     p.passes = (int)cdiv(p.rows, p.n_rows);
     p.n_pad = p.n_rows * kDigits;
-    // Up to 16 rows two CTAs share an SM (256 tensor-memory columns and at most 113 KB each).  Each
-    // takes more than a third of the SM's shared memory, so that a third CTA never waits there for
-    // tensor memory while its cluster waits for it.
-    const bool small = p.n_rows <= 16;
     p.d_cols = (int)cdiv(p.n_pad, 32) * 32;
-    p.tmem_cols = small ? 256 : 512;
-    const int stage = (int)(kRowsCodeBytes + kRowsScaleBytes) + p.n_pad * 128;
-    // as many parts of the channels as still let every CTA be resident at once
-    const int tiles = p.Co / 128 * p.passes, places = small ? 296 : 148;
-    p.splits = 1;
-    while (p.splits < 8 && tiles * p.splits * 2 <= places && p.splits * 2 <= p.Ci / 256) p.splits *= 2;
-    const int room = (small ? kSmallSmem : kMaxSmem) - 1024;
-    p.stages_a = imin(imin(kRowsStages, room / stage), (p.tmem_cols - p.d_cols - (int)cdiv(p.n_rows, 16) * 16 - 8) / 16);
-    p.smem = p.stages_a * stage + 1024;
-    if (p.smem < 80 * 1024) p.smem = 80 * 1024;
+    const int tiles = p.Co / 128 * p.passes, k256 = p.Ci / 256, low = p.slab / 64;
+    const int stage_w = (int)(kRowsCodeBytes + kRowsScaleBytes), digits = p.n_pad * 128;
+    // Up to 16 rows two CTAs share an SM (256 tensor-memory columns and half the shared memory each; a third
+    // never fits, so none waits there for tensor memory while its cluster waits for it).  A cluster
+    // splits the channels as far as all CTAs are still resident at once.  Rows up to kRowsOwn get their digits
+    // from the product itself if those and a ring of enough stages fit, on half an SM or else on a whole one.
+    for (int attempt = 0; attempt < 4; attempt++) {
+        const bool own = attempt < 2, small = attempt % 2 == 0;
+        if ((own && p.rows > kRowsOwn) || (small && p.n_rows > 16)) continue;
+        p.splits = 1;
+        const int tries[] = {8, 6, 4, 3, 2};
+        for (int s : tries) {
+            int clusters = 0;
+            cudaError_t e = s <= k256 ? resident_clusters(small, s, &clusters) : cudaSuccess;
+            if (e != cudaSuccess) return e;
+            if (s <= k256 && tiles <= clusters) {
+                p.splits = s;
+                break;
+            }
+        }
+        const int nA = (int)cdiv(k256, p.splits);
+        p.own_digits = own;
+        p.tmem_cols = small ? 256 : 512;
+        p.smem = small ? kSmallSmem : kMaxSmem;
+        const int room = p.smem - 1024 - (own ? nA * digits : 0), stage = stage_w + (own ? 0 : digits);
+        p.stages_a = room < 0 ? 0 : imin(imin(kRowsStages, room / stage), (p.tmem_cols - p.d_cols - (int)cdiv(p.n_rows, 16) * 16 - 8) / 16);
+        if (!own || p.stages_a >= imin(small ? 4 : 6, nA + low)) break;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t launch_rows_fp4(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const CUtensorMap& tm_x, const CUtensorMap& tm_l2,
                             const CUtensorMap& tm_u, const RowsParams& p, cudaStream_t st) {
     cudaError_t e = launch_rows_prepare(p, true, st);
     if (e != cudaSuccess) return e;
-    e = once_per_device((const void*)k_rows_fp4, [] {
-        return cudaFuncSetAttribute(k_rows_fp4, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    });
-    if (e != cudaSuccess) return e;
+    if ((e = set_attributes()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
