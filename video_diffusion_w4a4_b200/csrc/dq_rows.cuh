@@ -61,37 +61,64 @@ __device__ __forceinline__ void f16x2_values(uint32_t h2, float& lo, float& hi) 
     lo = f.x, hi = f.y;
 }
 
-// The next FP4 digit of each of eight values |v| <= 4 as packed codes: the nearest integers, which the values
-// then leave for the next digit, eight times finer.
-__device__ __forceinline__ uint32_t next_digits8(float (&v)[8]) {
+// The next FP4 digit of each of eight values |v| <= 4 (as four fp32 pairs) as packed codes: the nearest
+// integers, which the values then leave for the next digit, eight times finer.  Every step is exact.
+__device__ __forceinline__ uint32_t next_digits8(uint64_t (&v)[4]) {
+    const uint64_t magic = f2_pack(12582912.f, 12582912.f), eight = f2_pack(8.f, 8.f);   // 1.5 2^23
     float d[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        d[i] = __fsub_rn(__fadd_rn(v[i], 12582912.f), 12582912.f);
-        v[i] = (v[i] - d[i]) * 8.f;
+    for (int i = 0; i < 4; i++) {
+        const uint64_t n = f2_sub(f2_add(v[i], magic), magic);
+        v[i] = f2_mul(f2_sub(v[i], n), eight);
+        f2_unpack(n, d[2 * i], d[2 * i + 1]);
     }
     return cvt_e2m1x8(d);
 }
 
-// The values of eight consecutive channels from c on of row m
+// Eight channels of a row as they lie in memory, and their values
 template <int kFmt>
-__device__ __forceinline__ void load_values8(const RowsParams& p, int m, int c, float (&v)[8]) {
+struct Raw8 {
+    uint32_t w[kFmt == DQ_ROWS_BF16 ? 4 : 2];
+    float s;   // the scale of their 64 channels
+};
+
+// Channels c to c + 7 of row m
+template <int kFmt>
+__device__ __forceinline__ Raw8<kFmt> load_raw8(const RowsParams& p, int m, int c) {
+    Raw8<kFmt> r;
     const long long off = (long long)m * p.x_stride + c;
     if (kFmt == DQ_ROWS_BF16) {
         const uint4 a = *reinterpret_cast<const uint4*>((const uint16_t*)p.x + off);
-        const uint32_t r[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; i++) v[2 * i] = bf16_lo(r[i]), v[2 * i + 1] = bf16_hi(r[i]);
+        r.w[0] = a.x, r.w[1] = a.y, r.w[kFmt == DQ_ROWS_BF16 ? 2 : 0] = a.z, r.w[kFmt == DQ_ROWS_BF16 ? 3 : 0] = a.w;
     } else {
         const uint2 a = *reinterpret_cast<const uint2*>((const uint8_t*)p.x + off);
-        const uint32_t r[2] = {a.x, a.y};
-        const float s = kFmt == DQ_ROWS_E4M3_GROUP64 ? p.x_scales[(long long)m * (p.Ci / 64) + c / 64] : 1.f;
+        r.w[0] = a.x, r.w[1] = a.y;
+    }
+    r.s = kFmt == DQ_ROWS_E4M3_GROUP64 ? p.x_scales[(long long)m * (p.Ci / 64) + c / 64] : 1.f;
+    return r;
+}
+
+template <int kFmt>
+__device__ __forceinline__ void values8(const Raw8<kFmt>& r, float (&v)[8]) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            f16x2_values(e4m3x2_to_f16x2(r[i / 2] >> (16 * (i & 1))), v[2 * i], v[2 * i + 1]);
-            if (kFmt == DQ_ROWS_E4M3_GROUP64) v[2 * i] *= s, v[2 * i + 1] *= s;
+    for (int i = 0; i < 4; i++) {
+        if (kFmt == DQ_ROWS_BF16) {
+            v[2 * i] = bf16_lo(r.w[i % (kFmt == DQ_ROWS_BF16 ? 4 : 2)]), v[2 * i + 1] = bf16_hi(r.w[i % (kFmt == DQ_ROWS_BF16 ? 4 : 2)]);
+        } else {
+            f16x2_values(e4m3x2_to_f16x2(r.w[i / 2] >> (16 * (i & 1))), v[2 * i], v[2 * i + 1]);
+            if (kFmt == DQ_ROWS_E4M3_GROUP64) v[2 * i] *= r.s, v[2 * i + 1] *= r.s;
         }
     }
+}
+
+template <int kFmt>
+__device__ __forceinline__ float amax8(const Raw8<kFmt>& r) {
+    float v[8];
+    values8<kFmt>(r, v);
+    float a = fabsf(v[0]);
+#pragma unroll
+    for (int i = 1; i < 8; i++) a = max_nan(a, fabsf(v[i]));
+    return a;
 }
 
 // Exponent k of a row's power of two E = 2^k from its largest magnitude: the first digit's unit (values
@@ -113,6 +140,13 @@ struct Scale2 {
 __device__ __forceinline__ Scale2 inv_scale(int k) {
     const int h = (-k) / 2;
     return Scale2{pow2i(h), pow2i(-k - h)};
+}
+
+// v 2^-k for eight values (zeros for a row that is not finite: its factor is NaN)
+__device__ __forceinline__ void scaled_pairs(const float (&v)[8], Scale2 s, bool finite, uint64_t (&o)[4]) {
+    const uint64_t a = f2_pack(s.a, s.a), b = f2_pack(s.b, s.b);
+#pragma unroll
+    for (int i = 0; i < 4; i++) o[i] = finite ? f2_mul(f2_mul(f2_pack(v[2 * i], v[2 * i + 1]), a), b) : 0ull;
 }
 
 // A place in a ring and the parity of its use, stepped without a division (a division by a runtime

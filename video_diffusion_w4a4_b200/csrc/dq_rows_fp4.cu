@@ -37,10 +37,12 @@ constexpr int kDigits = kRowsDigits;
 
 constexpr int kMainThreads = 384;               // producers of A and B, MMA, a spare warp, eight epilogue warps
 constexpr int kEpiThreads = 256;
-constexpr int kMaxSmem = 225 * 1024, kSmallSmem = 225 * 512;   // dynamic shared memory, one CTA or two per SM
+constexpr int kMaxSmem = 225 * 1024, kSmallSmem = 112 * 1024;   // dynamic shared memory, one CTA or two per SM
+
+constexpr int kOwnTurns = 8;                    // pieces of eight channels a thread holds (own digits)
 
 struct Fp4Bars {
-    uint64_t full[kRowsStages], empty[kRowsStages], accf, digits;
+    uint64_t full[kRowsStages], empty[kRowsStages], accf, digits[kOwnTurns];
     float e[kRowsPass];   // the rows' factors
     float amax[8];        // own digits: each warp's part of its row's largest magnitude
     uint32_t tmem;
@@ -72,51 +74,58 @@ __device__ __forceinline__ void mma_nvfp4(uint32_t d_tmem, uint64_t adesc, uint6
 
 // Own digits (at most kRowsOwn rows): the epilogue warps, idle while the weight streams in, write the digits of
 // this CTA's channels into shared memory as the MMA reads them, with the power of two of the rows' values in these
-// channels alone.  Each row takes 8 / (rows rounded up to a power of two) warps.
+// channels alone.  Each row takes own_warps(rows) warps, which hold all its values from one read and write the
+// digits 256 channels a warp at a time, each such turn with a barrier of its own for the MMAs.
+__host__ __device__ constexpr int own_warps(int rows) { return rows == 1 ? 8 : rows == 2 ? 4 : rows <= 4 ? 2 : 1; }
+
 template <int kFmt>
 __device__ __forceinline__ void write_own_digits(const RowsParams& p, Fp4Bars& bars, uint8_t* dst, int c0, int channels) {
     const int ew = (int)(threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
-    const int per = p.rows == 1 ? 8 : p.rows == 2 ? 4 : p.rows <= 4 ? 2 : 1, m = ew / per, part = ew % per;
-    float v[8], am = 0.f;
-    if (m < p.rows) {
-#pragma unroll 4
-        for (int c = (part * 32 + lane) * 8; c < channels; c += per * 256) {
-            load_values8<kFmt>(p, m, c0 + c, v);
+    const int per = own_warps(p.rows), m = ew / per, part = ew % per, first = (part * 32 + lane) * 8;
+    Raw8<kFmt> raw[kOwnTurns];
+    float am = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; i++) am = max_nan(am, fabsf(v[i]));
-        }
+    for (int i = 0; i < kOwnTurns; i++) {
+        raw[i] = {};
+        if (m < p.rows && first + i * per * 256 < channels) raw[i] = load_raw8<kFmt>(p, m, c0 + first + i * per * 256);
     }
+#pragma unroll
+    for (int i = 0; i < kOwnTurns; i++) am = max_nan(am, amax8<kFmt>(raw[i]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
     if (lane == 0) bars.amax[ew] = am;
     bar_sync(1, kEpiThreads);
-    if (m < p.rows) {
-        for (int i = 0; i < per; i++) am = max_nan(am, bars.amax[m * per + i]);
-        const bool finite = finite_row(am);
-        const int k = row_unit<kFmt, true>(am);
-        if (part == 0 && lane == 0) {
-            float E = k >= -126 ? pow2i(k) : __int_as_float(1 << (k + 149));
-            if (kFmt == DQ_ROWS_E4M3) E *= p.x_scales[m];
-            bars.e[m] = finite ? E : __int_as_float(0x7FC00000);
-        }
-        const Scale2 s = inv_scale(k);
-#pragma unroll 2
-        for (int c = (part * 32 + lane) * 8; c < channels; c += per * 256) {
-            load_values8<kFmt>(p, m, c0 + c, v);
+    for (int i = 0; i < per; i++) am = max_nan(am, bars.amax[m * per + i]);
+    const bool finite = finite_row(am);
+    const int k = row_unit<kFmt, true>(am);
+    if (m < p.rows && part == 0 && lane == 0) {
+        float E = k >= -126 ? pow2i(k) : __int_as_float(1 << (k + 149));
+        if (kFmt == DQ_ROWS_E4M3) E *= p.x_scales[m];
+        bars.e[m] = finite ? E : __int_as_float(0x7FC00000);
+    }
+    const Scale2 s = inv_scale(k);
 #pragma unroll
-            for (int i = 0; i < 8; i++) v[i] = finite ? v[i] * s.a * s.b : 0.f;
-            // column 8 m + q of the 256-channel stage c / 256: row 8 m + q of 128 bytes, its 16-byte pieces
-            // permuted by the row's low bits (128-byte swizzle)
-            uint8_t* row = dst + (size_t)(c >> 8) * p.n_pad * 128 + m * 1024 + ((c >> 1) & 15);
-            const int piece = (c >> 5) & 7;
+    for (int i = 0; i < kOwnTurns; i++) {
+        const int c = first + i * per * 256;
+        if (i * per * 256 < channels) {
+            if (m < p.rows && c < channels) {
+                float v[8];
+                uint64_t v2[4];
+                values8<kFmt>(raw[i], v);
+                scaled_pairs(v, s, finite, v2);
+                // column 8 m + q of the 256-channel stage c / 256: row 8 m + q of 128 bytes, its 16-byte pieces
+                // permuted by the row's low bits (128-byte swizzle)
+                uint8_t* row = dst + (size_t)(c >> 8) * p.n_pad * 128 + m * 1024 + ((c >> 1) & 15);
+                const int piece = (c >> 5) & 7;
 #pragma unroll
-            for (int q = 0; q < kDigits; q++)
-                *reinterpret_cast<uint32_t*>(row + q * 128 + ((piece ^ q) << 4)) = next_digits8(v);
+                for (int q = 0; q < kDigits; q++)
+                    *reinterpret_cast<uint32_t*>(row + q * 128 + ((piece ^ q) << 4)) = next_digits8(v2);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the MMA reads them
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.digits[i]);
         }
     }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the MMA reads them
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bars.digits);
     bar_sync(1, kEpiThreads);   // the factors, for every epilogue warp
 }
 
@@ -148,7 +157,7 @@ __global__ void __launch_bounds__(kMainThreads, 2)
             mbar_init(&bars.empty[s], 1);
         }
         mbar_init(&bars.accf, 1);
-        mbar_init(&bars.digits, kEpiThreads / 32);
+        for (int i = 0; i < kOwnTurns; i++) mbar_init(&bars.digits[i], kEpiThreads / 32);
         bars.abort_flag = 0;
         fence_barrier_init();
     }
@@ -223,13 +232,17 @@ __global__ void __launch_bounds__(kMainThreads, 2)
         const uint32_t idesc = idesc_nvfp4(128, p.n_pad), id_low = idesc_bf16(128, (int)n16);
         const uint32_t base = smem_u32(sm);
         bar_sync(2, 32 + 128);   // the digits' scales are in tensor memory
-        bool alive = true;
-        if (own) alive = __all_sync(0xffffffffu, mbar_wait_spin(&bars.digits, 0, abort_flag, p.status, p.budget_ns));
         tc_fence_after();
         Ring r;
         uint32_t sa = base, ta = t_sf, sb = own ? smem_u32(digits) : base + kRowsCodeBytes;
         const uint32_t b_step = own ? b_all : stage;
-        for (int g = 0; alive && g < total; g++) {
+        int turn = 0, left = 0;                          // own digits: stages until the next turn's barrier
+        for (int g = 0; g < total; g++) {
+            if (own && g < nA && left-- == 0) {
+                if (!__all_sync(0xffffffffu, mbar_wait_spin(&bars.digits[turn], 0, abort_flag, p.status, p.budget_ns))) break;
+                turn++;
+                left = own_warps(p.rows) - 1;
+            }
             if (!__all_sync(0xffffffffu, mbar_wait_spin(&bars.full[r.slot], r.phase, abort_flag, p.status, p.budget_ns))) break;
             tc_fence_after();
             if (elect_one()) {
@@ -268,9 +281,8 @@ __global__ void __launch_bounds__(kMainThreads, 2)
     const int quad = warp & 3, group = (warp - 4) >> 2, row = quad * 32 + lane, et = tid - 128;
     const uint32_t trow = (uint32_t)(quad * 32) << 16;
     const PackedHeader* hdr = reinterpret_cast<const PackedHeader*>(p.packed_w);
-    const float S_W = hdr->S_W;
     bool done = true, ok = true;
-    float bv = 0.f;
+    float bv = 0.f, S_W = 0.f;
     if (warp >= 4) {
         if (warp < 8) {
             // the digits' scales: E4M3 1 in eight columns of every lane
@@ -282,8 +294,6 @@ __global__ void __launch_bounds__(kMainThreads, 2)
             __syncwarp();
             asm volatile("bar.arrive 2, 160;" ::: "memory");
         }
-        ok = header_ok(p);
-        if (hdr->flags & kPackedHasBias) bv = *(const float*)(p.packed_w + p.off_bias + 4ll * (o0 + row));
         if (own) {
             uint8_t* dst = digits;
             if (p.x_format == DQ_ROWS_BF16)
@@ -297,6 +307,9 @@ __global__ void __launch_bounds__(kMainThreads, 2)
             if (et < nm) bars.e[et] = p.e[m0 + et];
             bar_sync(1, kEpiThreads);
         }
+        ok = header_ok(p);
+        S_W = hdr->S_W;
+        if (hdr->flags & kPackedHasBias) bv = *(const float*)(p.packed_w + p.off_bias + 4ll * (o0 + row));
         if (lane == 0) done = mbar_wait(&bars.accf, 0, abort_flag, p.status, p.budget_ns);
         done = __shfl_sync(0xffffffffu, done, 0);
         tc_fence_after();
@@ -447,7 +460,7 @@ cudaError_t rows_fp4_plan(RowsParams& p) {
         p.smem = small ? kSmallSmem : kMaxSmem;
         const int room = p.smem - 1024 - (own ? nA * digits : 0), stage = stage_w + (own ? 0 : digits);
         p.stages_a = room < 0 ? 0 : imin(imin(kRowsStages, room / stage), (p.tmem_cols - p.d_cols - (int)cdiv(p.n_rows, 16) * 16 - 8) / 16);
-        if (!own || p.stages_a >= imin(small ? 4 : 6, nA + low)) break;
+        if (!own || (p.stages_a >= imin(small ? 4 : 6, nA + low) && nA <= kOwnTurns * own_warps(p.rows))) break;
     }
     return cudaSuccess;
 }

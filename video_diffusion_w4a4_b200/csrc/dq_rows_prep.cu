@@ -1,7 +1,7 @@
 // What the few-row products need of their rows (dq_rows_forward): the B operand
 // and the low-rank factor's intermediate U = xv L1, in one launch.
 //
-//   B operand, by blocks of 2048 channels of a row.
+//   B operand, by blocks of 4096 channels of a row.
 //     FP4 form   eight digits a value (dq_rows_fp4.cu) and the first digit's unit
 //     FP16 form  the value divided by a power of two E of its row, in FP16
 //                (dq_rows.cu), with a scale per 64 channels as hi + lo halves
@@ -23,19 +23,17 @@ namespace dq {
 
 namespace {
 
-constexpr int kThreads = 256, kCluster = 8, kBlockChannels = 8 * kThreads;
+constexpr int kThreads = 512, kCluster = 8, kBlockChannels = 8 * kThreads;
 
 template <int kFmt, bool kDigitForm>
 __device__ __forceinline__ void convert_block(const RowsParams& p, int m, int part) {
     __shared__ float sh[kThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, c = part * kBlockChannels + tid * 8;
-    float v[8], am = 0.f;
-    for (int i = tid * 8; i < p.Ci; i += kBlockChannels) {
-        load_values8<kFmt>(p, m, i, v);
-#pragma unroll
-        for (int e = 0; e < 8; e++) am = max_nan(am, fabsf(v[e]));
-    }
-    if (c < p.Ci) load_values8<kFmt>(p, m, c, v);
+    float am = 0.f;
+    Raw8<kFmt> raw = {};
+    if (c < p.Ci) raw = load_raw8<kFmt>(p, m, c);
+    for (int i = tid * 8; i < p.Ci; i += kBlockChannels) am = max_nan(am, amax8<kFmt>(load_raw8<kFmt>(p, m, i)));
+    griddep_launch();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
     if (lane == 0) sh[tid >> 5] = am;
@@ -51,18 +49,22 @@ __device__ __forceinline__ void convert_block(const RowsParams& p, int m, int pa
         p.e[m] = finite ? E : __int_as_float(0x7FC00000);   // a NaN or an infinity: NaN all over the row
     }
     if (c >= p.Ci) return;
-    const Scale2 s = inv_scale(k);
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = finite ? v[i] * s.a * s.b : 0.f;
+    float v[8];
+    uint64_t v2[4];
+    values8<kFmt>(raw, v);
+    scaled_pairs(v, inv_scale(k), finite, v2);
     if (kDigitForm) {
         uint8_t* dst = (uint8_t*)p.xh + (size_t)m * kRowsDigits * (p.Ci / 2) + c / 2;
 #pragma unroll
-        for (int q = 0; q < kRowsDigits; q++) *reinterpret_cast<uint32_t*>(dst + (size_t)q * (p.Ci / 2)) = next_digits8(v);
+        for (int q = 0; q < kRowsDigits; q++) *reinterpret_cast<uint32_t*>(dst + (size_t)q * (p.Ci / 2)) = next_digits8(v2);
     } else {
         uint16_t* dst = p.xh + (size_t)m * (p.hilo ? 2 * p.Ci : p.Ci) + c;
         uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; j++) w[j] = f16x2_rn(v[2 * j], v[2 * j + 1]);
+        for (int j = 0; j < 4; j++) {
+            f2_unpack(v2[j], v[2 * j], v[2 * j + 1]);
+            w[j] = f16x2_rn(v[2 * j], v[2 * j + 1]);
+        }
         *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
         if (kFmt == DQ_ROWS_E4M3_GROUP64) {
 #pragma unroll
@@ -106,19 +108,25 @@ __device__ __forceinline__ void load_rows_16(const RowsParams& p, int m0, int nm
 
 template <int kFmt, bool kDigitForm>
 __device__ __forceinline__ void lowrank_cluster(const RowsParams& p, int index) {
-    __shared__ float wpart[4][16][32], part[16][32], wmax[4][16], cmax[16];
+    __shared__ float wpart[8][16][32], part[16][32], wmax[8][16], cmax[16];
     __shared__ int rexp[16];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int crank = (int)cluster_ctarank(), rgroups = (p.rank + 31) / 32;
     const int m0 = index / rgroups * 16, nm = imin(16, p.rows - m0), j0 = index % rgroups * 32;
     const int nblk = p.Ci / 64, b0 = nblk * crank / kCluster, b1 = nblk * (crank + 1) / kCluster;
-    // a warp takes 16 of the ranks and every fourth 64-channel block; lane t of a quad owns 16 channels of
+    // a warp takes 16 of the ranks and every eighth 64-channel block; lane t of a quad owns 16 channels of
     // a block (any assignment of channels to the MMA's k is right as long as both operands use it)
     const int jw = j0 + 16 * (warp & 1), ks = warp >> 1;
     const bool active = jw < p.rank;
+    // L1's part for this CTA on its way before the product is let in: its streams of weights would come first
+    for (int e = tid; e < imin(32, p.rank - j0) * (b1 - b0); e += kThreads) {
+        const uint16_t* src = p.l1 + (long long)(j0 + e / (b1 - b0)) * p.Ci + (b0 + e % (b1 - b0)) * 64;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+    }
+    griddep_launch();
     float acc[2][4] = {}, am[2] = {0.f, 0.f};
 #pragma unroll 2
-    for (int b = b0 + ks; b < b1; b += 4) {
+    for (int b = b0 + ks; b < b1; b += 8) {
         uint32_t xa[2][8];
         float sc[2];
         load_rows_16<kFmt>(p, m0, nm, b, g, t, xa, sc);
@@ -165,10 +173,18 @@ __device__ __forceinline__ void lowrank_cluster(const RowsParams& p, int index) 
         }
     }
     __syncthreads();
-    for (int e = tid; e < 512; e += kThreads)
-        part[e >> 5][e & 31] = (wpart[0][e >> 5][e & 31] + wpart[1][e >> 5][e & 31]) + (wpart[2][e >> 5][e & 31] + wpart[3][e >> 5][e & 31]);
-    if (!kDigitForm && kFmt != DQ_ROWS_E4M3 && tid < 16)
-        cmax[tid] = max_nan(max_nan(wmax[0][tid], wmax[1][tid]), max_nan(wmax[2][tid], wmax[3][tid]));
+    {
+        const int m = tid >> 5;
+        float u = 0.f, a = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; k++) u += wpart[k][m][lane];
+        part[m][lane] = u;
+        if (!kDigitForm && kFmt != DQ_ROWS_E4M3 && tid < 16) {
+#pragma unroll
+            for (int k = 0; k < 8; k++) a = max_nan(a, wmax[k][tid]);
+            cmax[tid] = a;
+        }
+    }
     cluster_sync();
     if (!kDigitForm) {
         if (tid < 16) {
@@ -206,7 +222,6 @@ __device__ __forceinline__ void lowrank_cluster(const RowsParams& p, int index) 
 template <int kFmt, bool kDigitForm>
 __global__ void __launch_bounds__(kThreads) k_rows_prepare(RowsParams p) {
     griddep_wait();     // the launch before this one may still read the workspace, or write X
-    griddep_launch();
     const int parts = (p.Ci + kBlockChannels - 1) / kBlockChannels, blocks = p.own_digits ? 0 : p.rows * parts;
     const int first = (blocks + kCluster - 1) / kCluster * kCluster, b = (int)blockIdx.x;
     if (b == first && threadIdx.x == 0) *p.status = header_ok(p) ? 0 : kStatusBadWeight;
