@@ -22,8 +22,8 @@ ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fopenmp,-ffp-contract=off",
           "-I" + os.path.join(ROOT, "include")]
 SOURCES = ["dq_host.cpp", "dq_api.cu", "dq_quant.cu", "dq_gemm.cu", "dq_diag.cu", "dq_noalloc.cu",
-           "dq_norm.cu", "dq_rows.cu", "dq_rows_fp4.cu", "dq_rows_prep.cu"]
-HEADERS = ["dq_common.h", "dq_internal.h", "dq_ptx.cuh", "dq_rows.cuh"]
+           "dq_norm.cu", "dq_rows.cu"]
+HEADERS = ["dq_common.h", "dq_internal.h", "dq_ptx.cuh"]
 
 
 def _stale(target: str, deps: list[str]) -> bool:

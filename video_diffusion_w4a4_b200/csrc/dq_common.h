@@ -229,10 +229,9 @@ DQ_HD WsLayout ws_layout(const Geom& g, int Ci, int Co, int rank, int kgroup = 0
 }
 
 // Workspace of dq_rows_forward: the status word, the rows' factors (fp32), U as BF16 hi + lo (rows x
-// slab) and the product's B operand, four bytes a value: eight FP4 digits, or FP16 (hi and lo halves
-// with a scale per 64 channels).
+// slab) and the rows' FP4 digits (eight a value).
 struct RowsLayout {
-    size_t total, off_status, off_e, off_u, off_xh;
+    size_t total, off_status, off_e, off_u, off_digits;
 };
 
 DQ_HD RowsLayout rows_layout(int rows, int Ci, int rank) {
@@ -241,7 +240,7 @@ DQ_HD RowsLayout rows_layout(int rows, int Ci, int rank) {
     L.off_status = off;  off = align_up(off + 16, kAlign);
     L.off_e = off;       off = align_up(off + (size_t)rows * 4, kAlign);
     L.off_u = off;       off = align_up(off + (size_t)rows * slab_width(rank) * 2, kAlign);
-    L.off_xh = off;      off = align_up(off + (size_t)rows * Ci * 4, kAlign);
+    L.off_digits = off;  off = align_up(off + (size_t)rows * Ci * 4, kAlign);
     L.total = off;
     return L;
 }

@@ -133,27 +133,17 @@ struct RowsParams {
     const uint16_t* l2;         // Co x slab
     uint16_t* y;
     int* status;
-    float* e;                   // rows: factor of each row of xh
-    uint16_t* xh;               // rows x Ci FP16 (rows x 2 Ci with hilo): the product's B operand
-    uint16_t* u;                // rows x slab BF16: X L1 as hi + lo (over e S_W for the FP16 product)
-    int hilo;                   // xh holds hi and lo halves (a scale per 64 channels)
+    uint8_t* digits;            // rows x 8 x Ci/2: the rows' FP4 digits
+    uint16_t* u;                // rows x slab BF16: X L1 as hi + lo
+    float* e;                   // rows: what each row's sum of digits is multiplied by
     uint64_t budget_ns;
     // the cut of the product (rows_plan)
-    int n_rows, n_pad, passes;  // rows of X per pass, that rounded up to 16
-    int splits;                 // parts of the channels, one cluster per tile
-    int stages_a, stages_b, ring, smem, tmem_cols, d_cols;
-    int own_digits;             // FP4 product: its CTAs write the digits of their channels themselves
+    int n_rows, n_pad, passes;  // rows of X per pass, their digits' columns
+    int splits;                 // parts of the channels: the CTAs of a cluster
+    int stages, smem, tmem_cols, d_cols;
+    int own_digits;             // the product writes the digits itself
 };
-// Rows of X in FP4 digits (dq_rows_fp4.cu): digits per value, rows per pass
-constexpr int kRowsDigits = 8;
-constexpr int kRowsPass = 32;
-constexpr int kRowsFp4 = 64;
-constexpr int kRowsOwn = 8;   // rows whose digits the product's CTAs may write themselves
-cudaError_t rows_fp4_plan(RowsParams& p);
-cudaError_t launch_rows_fp4(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const CUtensorMap& tm_x, const CUtensorMap& tm_l2,
-                            const CUtensorMap& tm_u, const RowsParams& p, cudaStream_t st);
-cudaError_t launch_rows_prepare(const RowsParams& p, bool digit_form, cudaStream_t st);
-void rows_plan(RowsParams& p);
+cudaError_t rows_plan(RowsParams& p);
 cudaError_t launch_rows(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const CUtensorMap& tm_x,
                         const CUtensorMap& tm_l2, const CUtensorMap& tm_u, const RowsParams& p, cudaStream_t st);
 

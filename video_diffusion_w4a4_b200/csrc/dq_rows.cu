@@ -1,128 +1,500 @@
 // The product of few rows with a packed 4-bit weight (dq_rows_forward):
 //   Y[m] = act( S_W sum_c xv[m][c] (q s_b)[o][c] + (xv[m] L1) L2 + b )
 //
-// With few rows the weight's bytes bound it: they cross from HBM once, and
-// everything else hides behind that.  Two launches:
+// Few rows leave the weight's bytes as the bound, and decoding codes costs more
+// time than reading them.  Here they are not decoded: codes and group scales are
+// the A operand of kind::mxf4nvf4 as they lie in the packed weight, and a row of X
+// is written in the same format as kDigits = 8 FP4 digits a value,
+//   x = 2^(e-1) sum_p 8^-p d_p + r,   d_p in {-4, ..., 4},  |r| <= 2^(e-23),
+// with 2^e <= max |x| < 2^(e+1) over the row and d_p the nearest integer to what
+// the digits before it leave: 24 bits of the row's largest value, what an fp32 sum
+// over the row keeps of it.  Each digit is a column of the MMA (the B scales are 1)
+// and the epilogue sums a row's columns with their weights 8^-p in fp32.
 //
-//   k_rows_prepare  rows -> the B operand, and U = xv L1.  FP16 holds every
-//     q s_b exactly (6 significant bits, 2^-10 to 2688), so the product runs on
-//     kind::f16 with FP16 operands, and a BF16 row is moved into FP16's range
-//     by a power of two E of its own: x / E <= 2^15 keeps all 8 bits of values
-//     down to 2^-29 of the row's largest, and is off by at most 2^-40 of the
-//     largest below that, far under the fp32 sums' rounding.  E4M3 codes are
-//     FP16 values already (E = the row's scale); with a scale per 64 channels
-//     the row is code * scale, split into FP16 hi + lo (22 bits).  A cluster of
-//     eight CTAs takes 16 rows, an eighth of the channels each, and joins its
-//     maxima and its partial sums of U in a fixed order through distributed
-//     shared memory; U / (E S_W) is kept as BF16 hi + lo, as in the cube layer.
-//   k_rows_main     the product.  A CTA owns 128 output channels (the MMA's
-//     rows) and up to 256 rows of X (its columns), and a part of the channels
-//     when the tiles alone do not fill the GPU: the CTAs of a tile form a
-//     cluster and sum their parts in rank order.  Codes and scales arrive by
-//     TMA; eight warps turn them into FP16 (cvt.f16x2.e2m1x2, one product with
-//     the group's scale) and put them into tensor memory, the MMA's A operand:
-//     through shared memory they would cross it three times (write, and the
-//     MMA's reads), which alone would take longer than the weight takes from
-//     HBM.  The low-rank factor is extra BF16 K steps on the same accumulator.
-//     The weight's loads do not wait for k_rows_prepare (programmatic launch).
+// The low-rank factor is BF16 K steps of the same warp into columns of their own
+// (U = xv L1 as hi + lo, times L2).
+//
+//   k_rows_prepare   U, and digits and unit 2^(e-1) of each row (more than kOwnRows
+//                    rows; fewer are left to the product)
+//   k_rows_product   128 output channels (the MMA's M) times up to 32 rows (256
+//                    columns) per CTA.  One warp keeps codes and scales in flight,
+//                    one the digits, one issues scale copies and MMAs, eight write
+//                    the output (and before it, for the fewest rows, the digits).
+//                    When the tiles alone do not fill the GPU a cluster splits the
+//                    channels and sums its parts in order through distributed
+//                    shared memory.
+//
+// k_rows_product is launched while k_rows_prepare runs (programmatic launch): its
+// loads of the weight need only what was there before both.  Once they stream,
+// a load of anything else waits behind them for 2 to 4 us, a ring of the weight's
+// stages per SM deep; so the few other loads come first, or where nothing waits for
+// them, and k_rows_prepare lets the product in when its own have arrived, unless
+// only U is left to it, which the product needs last.
 #include "../../include/deltaquant.h"
 #include "dq_common.h"
 #include "dq_internal.h"
 #include "dq_ptx.cuh"
-#include "dq_rows.cuh"
+
+#include <atomic>
 
 namespace dq {
 
 namespace {
 
-// ------------------------------------------------------------------ PTX used by this file alone
+constexpr int kDigits = 8;                       // FP4 digits of a value
+constexpr int kPassRows = 32;                    // rows of X per CTA: 256 MMA columns
+constexpr int kOwnRows = 8;                      // up to so many rows the product writes the digits itself
+constexpr int kOwnTurns = 8;                     // pieces of eight channels a thread holds for that
+constexpr int kThreads = 384;                    // producers of A and B, MMA, a spare warp, eight epilogue warps
+constexpr int kEpiThreads = 256;
+constexpr int kStages = 16;                      // stages of the operand ring at most
+constexpr uint32_t kCodeBytes = 128 * 128;       // codes of 128 output channels x 256 input channels
+constexpr uint32_t kScaleBytes = 4 * 512;        // their group scales
+// Dynamic shared memory of a CTA that has an SM to itself, and of one of two that share it (a third
+// never fits, so none waits on an SM for tensor memory while its cluster waits for it).
+constexpr int kMaxSmem = 225 * 1024, kSmallSmem = 111 * 1024;
 
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// ------------------------------------------------------------------ small pieces
+
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// D(16 x 8) += A(16 x 16) B(16 x 8), BF16 operands, fp32 sums
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Each thread of the warp reads four consecutive 32-bit columns of its lane.
+__device__ __forceinline__ void tmem_ld_x4(uint32_t taddr, uint32_t (&r)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// 32 lanes x 16 bytes from shared memory to four columns of every 32-lane quadrant
+__device__ __forceinline__ void tmem_cp_32x128b(uint32_t taddr, uint64_t sdesc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+__device__ __forceinline__ void mma_nvfp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                          uint32_t sfb, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
         : "memory");
 }
 
-// kind::f16, FP16 x FP16 -> fp32, K-major operands
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
-    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// Two E4M3 codes -> FP16 pair (exact), the low byte's in the low half
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)codes));
+    return h2;
 }
 
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
+// 2^e for -126 <= e <= 127
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ bool header_ok(const RowsParams& p) {
+    const PackedHeader* h = reinterpret_cast<const PackedHeader*>(p.packed_w);
+    return h->magic == DQ_PACK_MAGIC && h->version == DQ_PACK_FORMAT_VERSION && h->Ci == p.Ci && h->Co == p.Co &&
+           h->rank == p.rank && h->slab == p.slab;
+}
+
+__device__ __forceinline__ void f16x2_values(uint32_t h2, float& lo, float& hi) {
+    __half2_raw r;
+    r.x = (uint16_t)(h2 & 0xFFFFu), r.y = (uint16_t)(h2 >> 16);
+    const float2 f = __half22float2(__half2(r));
+    lo = f.x, hi = f.y;
+}
+
+// One lane of a converged warp, the same every time
+__device__ __forceinline__ bool elect_one() {
+    uint32_t pred;
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(pred));
+    return pred != 0;
 }
 
-// Eight E2M1 codes (value 2i in the low nibble of byte i) times the FP16 pair s -> four FP16 pairs
-__device__ __forceinline__ void decode8(uint32_t w, uint32_t s, uint32_t* out) {
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        ".reg .b32 t0, t1, t2, t3;\n\t"
-        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 t0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 t1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 t2, b2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 t3, b3;\n\t"
-        "mul.rn.f16x2 %0, t0, %5;\n\t"
-        "mul.rn.f16x2 %1, t1, %5;\n\t"
-        "mul.rn.f16x2 %2, t2, %5;\n\t"
-        "mul.rn.f16x2 %3, t3, %5;\n\t}"
-        : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3])
-        : "r"(w), "r"(s));
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t cluster_addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_dsmem_f32(uint32_t cluster_addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+}
+
+// ------------------------------------------------------------------ rows and digits
+
+// The next FP4 digit of each of eight values |v| <= 4 (as four fp32 pairs) as packed codes: the nearest
+// integers, which the values then leave for the next digit, eight times finer.  Every step is exact.
+__device__ __forceinline__ uint32_t next_digits8(uint64_t (&v)[4]) {
+    const uint64_t magic = f2_pack(12582912.f, 12582912.f), eight = f2_pack(8.f, 8.f);   // 1.5 2^23
+    float d[8];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint64_t n = f2_sub(f2_add(v[i], magic), magic);
+        v[i] = f2_mul(f2_sub(v[i], n), eight);
+        f2_unpack(n, d[2 * i], d[2 * i + 1]);
+    }
+    return cvt_e2m1x8(d);
+}
+
+// Eight channels of a row as they lie in memory, and their values
+template <int kFmt>
+struct Raw8 {
+    uint32_t w[kFmt == DQ_ROWS_BF16 ? 4 : 2];
+    float s;   // the scale of their 64 channels
+};
+
+// Channels c to c + 7 of row m
+template <int kFmt>
+__device__ __forceinline__ Raw8<kFmt> load_raw8(const RowsParams& p, int m, int c) {
+    Raw8<kFmt> r;
+    const long long off = (long long)m * p.x_stride + c;
+    if (kFmt == DQ_ROWS_BF16) {
+        const uint4 a = *reinterpret_cast<const uint4*>((const uint16_t*)p.x + off);
+        r.w[0] = a.x, r.w[1] = a.y, r.w[kFmt == DQ_ROWS_BF16 ? 2 : 0] = a.z, r.w[kFmt == DQ_ROWS_BF16 ? 3 : 0] = a.w;
+    } else {
+        const uint2 a = *reinterpret_cast<const uint2*>((const uint8_t*)p.x + off);
+        r.w[0] = a.x, r.w[1] = a.y;
+    }
+    r.s = kFmt == DQ_ROWS_E4M3_GROUP64 ? p.x_scales[(long long)m * (p.Ci / 64) + c / 64] : 1.f;
+    return r;
+}
+
+template <int kFmt>
+__device__ __forceinline__ void values8(const Raw8<kFmt>& r, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        if (kFmt == DQ_ROWS_BF16) {
+            v[2 * i] = bf16_lo(r.w[i % (kFmt == DQ_ROWS_BF16 ? 4 : 2)]), v[2 * i + 1] = bf16_hi(r.w[i % (kFmt == DQ_ROWS_BF16 ? 4 : 2)]);
+        } else {
+            f16x2_values(e4m3x2_to_f16x2(r.w[i / 2] >> (16 * (i & 1))), v[2 * i], v[2 * i + 1]);
+            if (kFmt == DQ_ROWS_E4M3_GROUP64) v[2 * i] *= r.s, v[2 * i + 1] *= r.s;
+        }
+    }
+}
+
+template <int kFmt>
+__device__ __forceinline__ float amax8(const Raw8<kFmt>& r) {
+    float v[8];
+    values8<kFmt>(r, v);
+    float a = fabsf(v[0]);
+#pragma unroll
+    for (int i = 1; i < 8; i++) a = max_nan(a, fabsf(v[i]));
+    return a;
+}
+
+// Exponent of a row's unit, the weight of its first digit, from its largest magnitude: values stay below 4
+// units; subnormals count as 2^-126.
+__device__ __forceinline__ int unit_exponent(float am) {
+    const int e = (int)((__float_as_uint(am) >> 23) & 255);
+    return (e ? e - 127 : -126) - 1;
+}
+
+// What a row's sum of digits is multiplied by: its unit 2^k, with the row's scale where the format has one; NaN
+// for a row with a NaN or an infinity, whose digits are zeros.
+template <int kFmt>
+__device__ __forceinline__ float row_factor(const RowsParams& p, int m, int k, bool finite) {
+    float E = k >= -126 ? pow2i(k) : __int_as_float(1 << (k + 149));
+    if (kFmt == DQ_ROWS_E4M3) E *= p.x_scales[m];
+    return finite ? E : __int_as_float(0x7FC00000);
+}
+
+__device__ __forceinline__ bool finite_row(float am) { return am < __int_as_float(0x7F800000); }
+
+// 2^-k in two exact steps (k in [-127, 126])
+struct Scale2 {
+    float a, b;
+};
+__device__ __forceinline__ Scale2 inv_scale(int k) {
+    const int h = (-k) / 2;
+    return Scale2{pow2i(h), pow2i(-k - h)};
+}
+
+// v 2^-k for eight values (zeros for a row that is not finite: its factor is NaN)
+__device__ __forceinline__ void scaled_pairs(const float (&v)[8], Scale2 s, bool finite, uint64_t (&o)[4]) {
+    const uint64_t a = f2_pack(s.a, s.a), b = f2_pack(s.b, s.b);
+#pragma unroll
+    for (int i = 0; i < 4; i++) o[i] = finite ? f2_mul(f2_mul(f2_pack(v[2 * i], v[2 * i + 1]), a), b) : 0ull;
+}
+
+// Channels 64 b + 16 t to + 15 of the rows m0 + g and m0 + g + 8 (the second unless kHalf) as BF16 pairs (zeros from
+// row nm on), and their scales where the format has one per 64 channels.
+template <int kFmt, bool kHalf>
+__device__ __forceinline__ void load_rows_16(const RowsParams& p, int m0, int nm, int b, int g, int t, uint32_t (&xa)[2][8],
+                                             float (&sc)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const int m = g + 8 * h;
+#pragma unroll
+        for (int i = 0; i < 8; i++) xa[h][i] = 0;
+        sc[h] = 0.f;
+        if ((kHalf && h) || m >= nm) continue;
+        const long long off = (long long)(m0 + m) * p.x_stride + b * 64 + t * 16;
+        if (kFmt == DQ_ROWS_BF16) {
+            const uint4* src = reinterpret_cast<const uint4*>((const uint16_t*)p.x + off);
+            const uint4 u = src[0], v = src[1];
+            xa[h][0] = u.x, xa[h][1] = u.y, xa[h][2] = u.z, xa[h][3] = u.w;
+            xa[h][4] = v.x, xa[h][5] = v.y, xa[h][6] = v.z, xa[h][7] = v.w;
+        } else {
+            const uint4 u = *reinterpret_cast<const uint4*>((const uint8_t*)p.x + off);
+            const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 8; i++) xa[h][i] = e4m3x2_to_bf16x2(q[i / 2] >> (16 * (i & 1)));
+        }
+        if (kFmt == DQ_ROWS_E4M3_GROUP64) sc[h] = p.x_scales[(long long)(m0 + m) * (p.Ci / 64) + b];
+    }
+}
+
+constexpr int kPrepThreads = 512, kPrepCluster = 8, kBlockChannels = 8 * kPrepThreads;
+
+// Digits of 4096 channels of a row.  Each block finds the row's largest magnitude for itself: a second read of at
+// most 28 KB, from L2, costs less than a hand-off between blocks.
+template <int kFmt>
+__device__ __forceinline__ void digits_block(const RowsParams& p, int m, int part) {
+    __shared__ float sh[kPrepThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, c = part * kBlockChannels + tid * 8;
+    float am = 0.f;
+    Raw8<kFmt> raw = {};
+    if (c < p.Ci) raw = load_raw8<kFmt>(p, m, c);
+    for (int i = tid * 8; i < p.Ci; i += kBlockChannels) am = max_nan(am, amax8<kFmt>(load_raw8<kFmt>(p, m, i)));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
+    if (lane == 0) sh[tid >> 5] = am;
+    __syncthreads();
+    griddep_launch();   // the block's loads have arrived
+    am = sh[0];
+#pragma unroll
+    for (int w = 1; w < kPrepThreads / 32; w++) am = max_nan(am, sh[w]);
+    const bool finite = finite_row(am);
+    const int k = unit_exponent(am);
+    if (part == 0 && tid == 0) p.e[m] = row_factor<kFmt>(p, m, k, finite);
+    if (c >= p.Ci) return;
+    float v[8];
+    uint64_t v2[4];
+    values8<kFmt>(raw, v);
+    scaled_pairs(v, inv_scale(k), finite, v2);
+    uint8_t* dst = p.digits + (size_t)m * kDigits * (p.Ci / 2) + c / 2;
+#pragma unroll
+    for (int q = 0; q < kDigits; q++) *reinterpret_cast<uint32_t*>(dst + (size_t)q * (p.Ci / 2)) = next_digits8(v2);
+}
+
+// U = xv L1 of 16 rows and 32 ranks by a cluster of eight CTAs, an eighth of the channels each: a warp takes 16 of
+// the ranks and every eighth 64-channel block, lane t of a quad 16 channels of a block (any assignment of channels
+// to the MMA's k is right that both operands share).  The sums are joined in rank order through distributed
+// shared memory and kept as BF16 hi + lo, 2^-17 of the value.
+template <int kFmt, bool kHalf>
+__device__ __forceinline__ void lowrank_cluster(const RowsParams& p, int index) {
+    __shared__ float wpart[8][16][32], part[16][32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int crank = (int)cluster_ctarank(), rgroups = (p.rank + 31) / 32;
+    const int m0 = index / rgroups * 16, nm = imin(16, p.rows - m0), j0 = index % rgroups * 32;
+    const int nblk = p.Ci / 64, b0 = nblk * crank / kPrepCluster, b1 = nblk * (crank + 1) / kPrepCluster;
+    const int jw = j0 + 16 * (warp & 1), ks = warp >> 1;
+    if (p.own_digits) {
+        // L1's part for this CTA on its way before the product is let in
+        for (int j = j0 + warp; j < imin(j0 + 32, p.rank); j += kPrepThreads / 32)
+            for (int b = b0 + lane; b < b1; b += 32)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.l1 + (long long)j * p.Ci + b * 64));
+        griddep_launch();
+    }
+    float acc[2][4] = {};
+    if (jw < p.rank) {
+#pragma unroll 2
+        for (int b = b0 + ks; b < b1; b += 8) {
+            uint32_t xa[2][8];
+            float sc[2];
+            load_rows_16<kFmt, kHalf>(p, m0, nm, b, g, t, xa, sc);
+#pragma unroll
+            for (int n = 0; n < 2; n++) {
+                const uint4* src = reinterpret_cast<const uint4*>(p.l1 + (long long)(jw + 8 * n + g) * p.Ci + b * 64 + t * 16);
+                const uint4 u = src[0], v = src[1];
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_16816(d, xa[0][0], xa[1][0], xa[0][1], xa[1][1], u.x, u.y);
+                mma_16816(d, xa[0][2], xa[1][2], xa[0][3], xa[1][3], u.z, u.w);
+                mma_16816(d, xa[0][4], xa[1][4], xa[0][5], xa[1][5], v.x, v.y);
+                mma_16816(d, xa[0][6], xa[1][6], xa[0][7], xa[1][7], v.z, v.w);
+                const float s0 = kFmt == DQ_ROWS_E4M3_GROUP64 ? sc[0] : 1.f, s1 = kFmt == DQ_ROWS_E4M3_GROUP64 ? sc[1] : 1.f;
+                acc[n][0] = fmaf(d[0], s0, acc[n][0]);
+                acc[n][1] = fmaf(d[1], s0, acc[n][1]);
+                acc[n][2] = fmaf(d[2], s1, acc[n][2]);
+                acc[n][3] = fmaf(d[3], s1, acc[n][3]);
+            }
+        }
+    }
+    // lane (g, t): rows g and g + 8, ranks 8 n + 2 t and the next of the warp's sixteen
+#pragma unroll
+    for (int n = 0; n < 2; n++) {
+        float* w0 = &wpart[ks][g][16 * (warp & 1) + 8 * n + 2 * t];
+        w0[0] = acc[n][0], w0[1] = acc[n][1];
+        w0[8 * 32] = acc[n][2], w0[8 * 32 + 1] = acc[n][3];
+    }
+    __syncthreads();
+    if (!p.own_digits) griddep_launch();   // the CTA's loads have arrived
+    {
+        float u = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; k++) u += wpart[k][warp][lane];
+        part[warp][lane] = u;
+    }
+    cluster_sync();
+    // an eighth of the sums per CTA: two rows
+    const int m = 2 * crank + (warp & 1), j = j0 + lane;
+    uint16_t* dst = p.u + (long long)(m0 + m) * p.slab;
+    if (warp < 2 && m < nm && j < p.rank) {
+        const uint32_t at = smem_u32(&part[m][lane]);
+        float v[kPrepCluster], u = 0.f;
+#pragma unroll
+        for (int c = 0; c < kPrepCluster; c++) v[c] = ld_dsmem_f32(mapa_shared(at, c));
+#pragma unroll
+        for (int c = 0; c < kPrepCluster; c++) u += v[c];
+        if (kFmt == DQ_ROWS_E4M3) u *= p.x_scales[m0 + m];
+        const uint16_t hi = f32_to_bf16_rn(u);
+        dst[j] = hi;
+        dst[p.rank + j] = f32_to_bf16_rn(u - bf16_lo(hi));
+    } else if ((warp >> 1) == 1 && m < nm && j0 == 0 && 2 * p.rank + lane < p.slab) {
+        dst[2 * p.rank + lane] = 0;   // zeros up to the slab's width (at most 32 columns)
+    }
+    cluster_sync();   // no CTA leaves while another still reads its sums
+}
+
+template <int kFmt>
+__global__ void __launch_bounds__(kPrepThreads) k_rows_prepare(RowsParams p) {
+    griddep_wait();     // the launch before this one may still read the workspace, or write X
+    const int parts = (p.Ci + kBlockChannels - 1) / kBlockChannels, blocks = p.own_digits ? 0 : p.rows * parts;
+    const int first = (blocks + kPrepCluster - 1) / kPrepCluster * kPrepCluster, b = (int)blockIdx.x;
+    if (b == first && threadIdx.x == 0) *p.status = header_ok(p) ? 0 : kStatusBadWeight;
+    if (b < blocks)
+        digits_block<kFmt>(p, b / parts, b % parts);
+    else if (b >= first && p.rows <= 8)
+        lowrank_cluster<kFmt, true>(p, (b - first) / kPrepCluster);
+    else if (b >= first)
+        lowrank_cluster<kFmt, false>(p, (b - first) / kPrepCluster);
 }
 
 // ------------------------------------------------------------------ the product
 
-constexpr int kMainThreads = 384;               // producers (A, B), MMA, a spare warp, eight decoding warps
-constexpr uint32_t kRowsStageA = kRowsCodeBytes + kRowsScaleBytes;   // 128 output x 256 input channels
-constexpr int kMaxSmem = 225 * 1024;             // dynamic shared memory of a CTA that has an SM to itself
+// A place in a ring and the parity of its use, stepped without a division (a division by a runtime
+// ring size costs more than a chunk's MMAs)
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int size) {
+        if (++slot == size) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
 
-struct MainBars {
-    uint64_t fullA[kRowsStages], emptyA[kRowsStages], fullB[kRowsStages], emptyB[kRowsStages], tfull[8], tempty[8], accf;
+struct Bars {
+    uint64_t full[kStages], empty[kStages], accf, digits[kOwnTurns];
+    float e[kPassRows];   // the rows' factors
+    float amax[8];        // own digits: each warp's part of its row's largest magnitude
     uint32_t tmem;
     int abort_flag;
 };
 
-__global__ void __launch_bounds__(kMainThreads, 2)
-    k_rows_main(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_s,
-                const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_l2,
-                const __grid_constant__ CUtensorMap tm_u, RowsParams p) {
+// Own digits: the epilogue warps write the digits of this CTA's channels into shared memory as the MMA reads
+// them, with the unit of the rows' values in these channels alone.  Each row takes own_warps(rows) warps, which
+// hold all its values from one read and write the digits 256 channels a warp at a time, each such turn with a
+// barrier of its own for the MMAs.
+__host__ __device__ constexpr int own_warps(int rows) { return rows == 1 ? 8 : rows == 2 ? 4 : rows <= 4 ? 2 : 1; }
+
+template <int kFmt>
+__device__ __forceinline__ void write_own_digits(const RowsParams& p, Bars& bars, uint8_t* dst, int c0, int channels) {
+    const int ew = (int)(threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
+    const int per = own_warps(p.rows), m = ew / per, part = ew % per, first = (part * 32 + lane) * 8;
+    Raw8<kFmt> raw[kOwnTurns];
+    float am = 0.f;
+#pragma unroll
+    for (int i = 0; i < kOwnTurns; i++) {
+        raw[i] = {};
+        if (m < p.rows && first + i * per * 256 < channels) raw[i] = load_raw8<kFmt>(p, m, c0 + first + i * per * 256);
+    }
+#pragma unroll
+    for (int i = 0; i < kOwnTurns; i++) am = max_nan(am, amax8<kFmt>(raw[i]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
+    if (lane == 0) bars.amax[ew] = am;
+    bar_sync(1, kEpiThreads);
+    for (int i = 0; i < per; i++) am = max_nan(am, bars.amax[m * per + i]);
+    const bool finite = finite_row(am);
+    const int k = unit_exponent(am);
+    if (m < p.rows && part == 0 && lane == 0) bars.e[m] = row_factor<kFmt>(p, m, k, finite);
+    const Scale2 s = inv_scale(k);
+#pragma unroll
+    for (int i = 0; i < kOwnTurns; i++) {
+        const int c = first + i * per * 256;
+        if (i * per * 256 < channels) {
+            if (m < p.rows && c < channels) {
+                float v[8];
+                uint64_t v2[4];
+                values8<kFmt>(raw[i], v);
+                scaled_pairs(v, s, finite, v2);
+                // column 8 m + q of the 256-channel stage c / 256: row 8 m + q of 128 bytes, its 16-byte pieces
+                // permuted by the row's low bits (128-byte swizzle)
+                uint8_t* row = dst + (size_t)(c >> 8) * p.n_pad * 128 + m * 1024 + ((c >> 1) & 15);
+                const int piece = (c >> 5) & 7;
+#pragma unroll
+                for (int q = 0; q < kDigits; q++)
+                    *reinterpret_cast<uint32_t*>(row + q * 128 + ((piece ^ q) << 4)) = next_digits8(v2);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the MMA reads them
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.digits[i]);
+        }
+    }
+}
+
+template <int kFmt, bool kOwn>
+__global__ void __launch_bounds__(kThreads, kOwn ? 2 : 1)
+    k_rows_product(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_s,
+                   const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_l2,
+                   const __grid_constant__ CUtensorMap tm_u, RowsParams p) {
     extern __shared__ __align__(16) uint8_t rows_smem[];
     uint8_t* sm = (uint8_t*)(((uintptr_t)rows_smem + 1023) & ~(uintptr_t)1023);
-    __shared__ MainBars bars;
+    __shared__ Bars bars;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int SA = p.stages_a, SB = p.stages_b, R = p.ring;
-    const uint32_t slotB = (uint32_t)p.n_pad * 128u;
-    uint8_t* ringB = sm + (size_t)SA * kRowsStageA;
-    volatile int* abort_flag = &bars.abort_flag;
-    const int split = (int)blockIdx.x, splits = (int)gridDim.x;       // the cluster spans a tile's splits
+    const int S = p.stages;
+    constexpr bool own = kOwn;
+    const int split = (int)blockIdx.x, splits = (int)gridDim.x;       // parts of the channels
     const int o0 = (int)blockIdx.y * 128;
     const int m0 = (int)blockIdx.z * p.n_rows;
     const int nm = imin(p.n_rows, p.rows - m0);
     const int k256 = p.Ci / 256, a0 = k256 * split / splits, nA = k256 * (split + 1) / splits - a0;
-    const int chunks = 4 * nA, tiles = p.hilo ? 2 : 1;
-    const int slabs = split == 0 ? p.slab / 64 : 0;
+    const uint32_t b_all = (uint32_t)p.n_pad * 128u, b_bytes = own ? 0u : b_all;   // digits of a stage; those in the ring
+    const uint32_t stage = kCodeBytes + b_bytes + kScaleBytes;        // codes, digits, the codes' scales
+    uint8_t* digits = sm + (size_t)S * stage;                         // own digits: [stage][column][128 bytes]
+    const int total = nA + (split == 0 ? p.slab / 64 : 0);            // stages: the weight's, then the low-rank factor's
+    const uint32_t n16 = (uint32_t)(p.n_rows + 15) & ~15u;
+    volatile int* abort_flag = &bars.abort_flag;
 
     if (tid == 0) {
-        for (int s = 0; s < SA; s++) {
-            mbar_init(&bars.fullA[s], 1);
-            mbar_init(&bars.emptyA[s], 16);   // four chunks of a stage, four warps each
+        for (int s = 0; s < S; s++) {
+            mbar_init(&bars.full[s], own ? 1 : 2);   // one producer, or both
+            mbar_init(&bars.empty[s], 1);
         }
-        for (int s = 0; s < SB; s++) {
-            mbar_init(&bars.fullB[s], 1);
-            mbar_init(&bars.emptyB[s], 1);
-        }
-        for (int s = 0; s < R; s++) {
-            mbar_init(&bars.tfull[s], 4);
-            mbar_init(&bars.tempty[s], 1);
-        }
+        for (int i = 0; i < kOwnTurns; i++) mbar_init(&bars.digits[i], kEpiThreads / 32);
         mbar_init(&bars.accf, 1);
         bars.abort_flag = 0;
         fence_barrier_init();
@@ -131,211 +503,215 @@ __global__ void __launch_bounds__(kMainThreads, 2)
         tmem_alloc(&bars.tmem, (uint32_t)p.tmem_cols);
         tmem_relinquish();
     }
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&tm_w);
+        prefetch_tmap(&tm_s);
+        prefetch_tmap(&tm_l2);
+        prefetch_tmap(&tm_u);
+        if (!own) prefetch_tmap(&tm_x);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = bars.tmem, ring0 = tmem + (uint32_t)p.d_cols;
+    const uint32_t tmem = bars.tmem, t_low = tmem + (uint32_t)p.d_cols, t_one = t_low + n16, t_sf = t_one + 8;
+    griddep_launch();
 
     if (warp == 0) {
-        // ------------------------------------------------ codes and scales, then the low-rank factor's rows
+        // ------------------------------------------------ codes and their scales
         if (lane == 0) {
-            const int total = nA + slabs, half = (o0 >> 7) & 1, blk0 = (o0 >> 8) * (p.Ci / 64) + a0 * 4;
+            const int half = (o0 >> 7) & 1, blk0 = (o0 >> 8) * (p.Ci / 64) + a0 * 4;
             Ring r;
             int g = 0;
-            for (; g < total; g++, r.next(SA)) {
-                uint64_t* full = &bars.fullA[r.slot];
-                if (g >= SA && !mbar_wait(&bars.emptyA[r.slot], r.phase ^ 1, abort_flag, p.status, p.budget_ns)) break;
-                uint8_t* dst = sm + (size_t)r.slot * kRowsStageA;
+            for (; g < total; g++, r.next(S)) {
+                uint64_t* full = &bars.full[r.slot];
+                if (g >= S && !mbar_wait(&bars.empty[r.slot], r.phase ^ 1, abort_flag, p.status, p.budget_ns)) break;
+                uint8_t* dst = sm + (size_t)r.slot * stage;
                 if (g < nA) {
-                    mbar_arrive_expect_tx(full, kRowsStageA);
+                    mbar_arrive_expect_tx(full, kCodeBytes + kScaleBytes);
                     tma_load_2d(dst, &tm_w, full, (a0 + g) * 128, o0);
                     // 32 lanes x 16 bytes per 64-channel block: one half of the 256-row tile
-                    tma_load_4d(dst + kRowsCodeBytes, &tm_s, full, 0, half, 0, blk0 + 4 * g);
+                    tma_load_4d(dst + kCodeBytes + b_bytes, &tm_s, full, 0, half, 0, blk0 + 4 * g);
                 } else {
-                    mbar_arrive_expect_tx(full, kRowsCodeBytes);
+                    // U lies in the place of the digits and the scales, 2 KB at least for 16 rows
+                    if (own && g == nA) griddep_wait();
+                    mbar_arrive_expect_tx(full, kCodeBytes + (own ? n16 * 128 : 0));
                     tma_load_2d(dst, &tm_l2, full, (g - nA) * 64, o0);
+                    if (own) tma_load_2d(dst + kCodeBytes, &tm_u, full, (g - nA) * 64, m0);
                 }
             }
-            for (int q = g > SA ? g - SA : 0; q < g; q++)   // every copy lands before shared memory is released
-                mbar_wait(&bars.fullA[q % SA], (uint32_t)(q / SA) & 1, abort_flag, nullptr, p.budget_ns, false);
+            for (int q = g > S ? g - S : 0; q < g; q++)   // every copy lands before shared memory is released
+                mbar_wait(&bars.full[q % S], (uint32_t)(q / S) & 1, abort_flag, nullptr, p.budget_ns, false);
         }
         __syncwarp();
     } else if (warp == 2) {
-        // ------------------------------------------------ rows of X (FP16), then U
-        if (lane == 0) {
+        // ------------------------------------------------ digits, then U
+        if (lane == 0 && !own) {
             griddep_wait();
-            const int main = chunks * tiles, total = main + slabs;
-            int x = a0 * 256, low = 0;
             Ring r;
             int g = 0;
-            for (; g < total; g++, r.next(SB)) {
-                uint64_t* full = &bars.fullB[r.slot];
-                if (g >= SB && !mbar_wait(&bars.emptyB[r.slot], r.phase ^ 1, abort_flag, p.status, p.budget_ns)) break;
-                mbar_arrive_expect_tx(full, slotB);
-                uint8_t* dst = ringB + (size_t)r.slot * slotB;
-                if (g < main) {
-                    tma_load_2d(dst, &tm_x, full, low + x, m0);
-                    low = tiles == 2 && low == 0 ? p.Ci : 0;   // hi, then lo of the same channels
-                    if (low == 0) x += 64;
-                } else {
-                    tma_load_2d(dst, &tm_u, full, (g - main) * 64, m0);
-                }
+            for (; g < total; g++, r.next(S)) {
+                uint64_t* full = &bars.full[r.slot];
+                if (g >= S && !mbar_wait(&bars.empty[r.slot], r.phase ^ 1, abort_flag, p.status, p.budget_ns)) break;
+                uint8_t* dst = sm + (size_t)r.slot * stage + kCodeBytes;
+                mbar_arrive_expect_tx(full, g < nA ? b_bytes : n16 * 128);
+                if (g < nA)
+                    tma_load_2d(dst, &tm_x, full, (a0 + g) * 128, m0 * kDigits);
+                else
+                    tma_load_2d(dst, &tm_u, full, (g - nA) * 64, m0);
             }
-            for (int q = g > SB ? g - SB : 0; q < g; q++)
-                mbar_wait(&bars.fullB[q % SB], (uint32_t)(q / SB) & 1, abort_flag, nullptr, p.budget_ns, false);
+            for (int q = g > S ? g - S : 0; q < g; q++)
+                mbar_wait(&bars.full[q % S], (uint32_t)(q / S) & 1, abort_flag, nullptr, p.budget_ns, false);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ MMAs (one elected lane; the warp's control flow is uniform)
-        const uint32_t id_main = idesc_f16(128, p.n_pad), id_slab = idesc_bf16(128, p.n_pad);
-        const uint64_t bdesc0 = desc_k_sw128(smem_u32(ringB));
-        Ring rt, rb;
-        bool alive = true;
-        for (int c = 0; alive && c < chunks; c++, rt.next(R)) {
-            if (!(alive = __all_sync(0xffffffffu, mbar_wait_spin(&bars.tfull[rt.slot], rt.phase, abort_flag, p.status, p.budget_ns)))) break;
-            const uint32_t at = ring0 + (uint32_t)(32 * rt.slot);
-            for (int h = 0; h < tiles; h++, rb.next(SB)) {
-                if (!(alive = __all_sync(0xffffffffu, mbar_wait_spin(&bars.fullB[rb.slot], rb.phase, abort_flag, p.status, p.budget_ns)))) break;
-                tc_fence_after();
-                const uint64_t bd = bdesc0 + (uint64_t)((uint32_t)rb.slot * (slotB >> 4));
-                if (elect_one()) {
-                    mma_f16_ts(tmem, at, bd, id_main, (c | h) != 0);
-                    mma_f16_ts(tmem, at + 8, bd + 2, id_main, 1u);
-                    mma_f16_ts(tmem, at + 16, bd + 4, id_main, 1u);
-                    mma_f16_ts(tmem, at + 24, bd + 6, id_main, 1u);
-                    tc_commit(&bars.emptyB[rb.slot]);
-                    if (h + 1 == tiles) tc_commit(&bars.tempty[rt.slot]);
-                }
-                __syncwarp();
+        const uint32_t idesc = idesc_nvfp4(128, p.n_pad), id_low = idesc_bf16(128, (int)n16);
+        const uint32_t base = smem_u32(sm);
+        bar_sync(2, 32 + 128);   // the digits' scales are in tensor memory
+        tc_fence_after();
+        Ring r;
+        uint32_t sa = base, ta = t_sf, sb = own ? smem_u32(digits) : base + kCodeBytes;
+        const uint32_t b_step = own ? b_all : stage;
+        int turn = 0, left = 0;                          // own digits: stages until the next turn's barrier
+        for (int g = 0; g < total; g++) {
+            if (own && g < nA && left-- == 0) {
+                if (!__all_sync(0xffffffffu, mbar_wait_spin(&bars.digits[turn], 0, abort_flag, p.status, p.budget_ns))) break;
+                turn++;
+                left = own_warps(p.rows) - 1;
             }
-        }
-        for (int i = 0; alive && i < slabs; i++, rb.next(SB)) {
-            const int ga = nA + i, sa = ga % SA;
-            if (!warp_wait(&bars.fullA[sa], (uint32_t)(ga / SA) & 1, abort_flag, p.status, p.budget_ns)) break;
-            if (!warp_wait(&bars.fullB[rb.slot], rb.phase, abort_flag, p.status, p.budget_ns)) break;
+            if (!__all_sync(0xffffffffu, mbar_wait_spin(&bars.full[r.slot], r.phase, abort_flag, p.status, p.budget_ns))) break;
             tc_fence_after();
-            const uint64_t ad = desc_k_sw128(smem_u32(sm + (size_t)sa * kRowsStageA));
-            const uint64_t bd = bdesc0 + (uint64_t)((uint32_t)rb.slot * (slotB >> 4));
             if (elect_one()) {
+                const uint64_t ad = desc_k_sw128(sa);
+                if (g < nA) {
+                    const uint64_t bd = desc_k_sw128(sb), fa = smem_desc(sa + kCodeBytes + b_bytes, 128, 128, 0);
+                    // the stage's own columns: nothing still reads them, as its empty barrier was waited for
 #pragma unroll
-                for (int k = 0; k < 4; k++) mma_bf16(tmem, ad + 2 * k, bd + 2 * k, id_slab, 1u);
-                tc_commit(&bars.emptyB[rb.slot]);
+                    for (int j = 0; j < 4; j++) tmem_cp_32x128b(ta + 4 * j, fa + 32 * j);
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        mma_nvfp4(tmem, ad + 2 * j, bd + 2 * j, idesc, ta + 4 * j, t_one, (g | j) != 0);
+                } else {
+                    const uint64_t bd = desc_k_sw128(sa + kCodeBytes);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) mma_bf16(t_low, ad + 2 * j, bd + 2 * j, id_low, (g > nA || j) ? 1u : 0u);
+                }
+                tc_commit(&bars.empty[r.slot]);
             }
             __syncwarp();
+            sa += stage, ta += 16, sb += b_step;
+            r.next(S);
+            if (r.slot == 0) {
+                sa = base, ta = t_sf;
+                if (!own) sb = base + kCodeBytes;
+            }
         }
         if (elect_one()) {
             tc_commit(&bars.accf);
             mbar_wait(&bars.accf, 0, abort_flag, nullptr, p.budget_ns, false);   // no MMA runs past this point
         }
         __syncwarp();
-    } else if (warp >= 4) {
-        // ------------------------------------------------ codes -> FP16 in tensor memory
-        const int quad = warp & 3, group = (warp - 4) >> 2;   // 32 output channels; every other 64-channel chunk
-        const int row = quad * 32 + lane;
-        const uint32_t trow = ring0 + ((uint32_t)(quad * 32) << 16);
-        // the TMA's 128-byte swizzle: 16-byte piece j of row r sits at piece j ^ (r % 8)
-        const uint32_t at = (uint32_t)row * 128, x16 = (uint32_t)(row & 7);
-        Ring ra, rt;
-        rt.slot = group;   // the ring's size is even: a group keeps to its places
-        for (int c = group; c < chunks; c += 2) {
-            if (!warp_wait(&bars.fullA[ra.slot], ra.phase, abort_flag, p.status, p.budget_ns)) break;
-            const uint8_t* st = sm + (size_t)ra.slot * kRowsStageA;
-            const uint32_t j0 = 2 * (c & 3);
-            const uint4 w0 = *reinterpret_cast<const uint4*>(st + at + ((j0 ^ x16) << 4));
-            const uint4 w1 = *reinterpret_cast<const uint4*>(st + at + (((j0 + 1) ^ x16) << 4));
-            const uint32_t sw = *reinterpret_cast<const uint32_t*>(st + kRowsCodeBytes + (c & 3) * 512 + lane * 16 + quad * 4);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.emptyA[ra.slot]);
-            const uint32_t s01 = e4m3x2_to_f16x2(sw), s23 = e4m3x2_to_f16x2(sw >> 16);
-            const uint32_t s0 = __byte_perm(s01, 0, 0x1010), s1 = __byte_perm(s01, 0, 0x3232);
-            const uint32_t s2 = __byte_perm(s23, 0, 0x1010), s3 = __byte_perm(s23, 0, 0x3232);
-            uint32_t v[16];
-            decode8(w0.x, s0, v), decode8(w0.y, s0, v + 4), decode8(w0.z, s1, v + 8), decode8(w0.w, s1, v + 12);
-            if (c >= R && !warp_wait(&bars.tempty[rt.slot], rt.phase ^ 1, abort_flag, p.status, p.budget_ns)) break;
-            tc_fence_after();
-            tmem_st_x16(trow + (uint32_t)(32 * rt.slot), v);
-            uint32_t u[16];
-            decode8(w1.x, s2, u), decode8(w1.y, s2, u + 4), decode8(w1.z, s3, u + 8), decode8(w1.w, s3, u + 12);
-            tmem_st_x16(trow + (uint32_t)(32 * rt.slot + 16), u);
+    }
+
+    // ---------------------------------------------------- epilogue warps
+    const int quad = warp & 3, group = (warp - 4) >> 2, row = quad * 32 + lane, et = tid - 128;
+    const uint32_t trow = (uint32_t)(quad * 32) << 16;
+    const PackedHeader* hdr = reinterpret_cast<const PackedHeader*>(p.packed_w);
+    bool done = true, ok = true;
+    float S_W = 0.f;
+    uint32_t flags = 0;
+    float bias = 0.f;
+    if (warp >= 4) {
+        flags = hdr->flags;
+        bias = *(const float*)(p.packed_w + p.off_bias + 4ll * (o0 + row));
+        S_W = hdr->S_W;
+        if (warp < 8) {
+            // the digits' scales: E4M3 1 in eight columns of every lane
+            const uint32_t one = 0x38383838u;
+            tmem_st_x4(t_one + trow, one, one, one, one);
+            tmem_st_x4(t_one + trow + 4, one, one, one, one);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.tfull[rt.slot]);
-            if ((c & 3) >= 2) ra.next(SA);
-            rt.slot += 2;
-            if (rt.slot >= R) rt.slot = group, rt.phase ^= 1;
+            asm volatile("bar.arrive 2, 160;" ::: "memory");
         }
-        __syncwarp();
-    }
-
-    // ---------------------------------------------------- epilogue
-    const bool ok = header_ok(p);
-    const PackedHeader* hdr = reinterpret_cast<const PackedHeader*>(p.packed_w);
-    const float S_W = hdr->S_W;
-    const float* bias = (hdr->flags & kPackedHasBias) ? (const float*)(p.packed_w + p.off_bias) : nullptr;
-    bool done = true;
-    if (warp >= 4) {
-        done = warp_wait(&bars.accf, 0, abort_flag, p.status, p.budget_ns);
+        if (own) {
+            write_own_digits<kFmt>(p, bars, digits, a0 * 256, nA * 256);
+        } else {
+            griddep_wait();   // the rows' factors come from k_rows_prepare
+            if (et < nm) bars.e[et] = p.e[m0 + et];
+        }
+        bar_sync(1, kEpiThreads);
+        ok = header_ok(p);
+        if (lane == 0) done = mbar_wait(&bars.accf, 0, abort_flag, p.status, p.budget_ns);
+        done = __shfl_sync(0xffffffffu, done, 0);
         tc_fence_after();
-        griddep_wait();   // the rows' factors come from k_rows_prepare
     }
-    const int quad = warp & 3, group = (warp - 4) >> 2, row = quad * 32 + lane;
-    // Y of one output channel and the rows m, m + 1 (the second where it exists)
-    auto finish = [&](int m, int o, float a0v, float a1v, float bv) {
-        const float e0 = p.e[m0 + m], e1 = m + 1 < nm ? p.e[m0 + m + 1] : 0.f;
-        float y0 = fmaf(a0v * S_W, e0, bv), y1 = fmaf(a1v * S_W, e1, bv);
+    const float bv = (flags & kPackedHasBias) ? bias : 0.f;
+    // This CTA's part of the rows 4 b to 4 b + 3 for the thread's output channel: the digits' columns with
+    // weights 8^-p, times S_W and the row's factor, and U L2 where this CTA has it
+    auto parts_of = [&](int b, float (&v)[4]) {
+        uint32_t acc[32], low[4];
+        if (split == 0) tmem_ld_x4(t_low + trow + (uint32_t)(4 * b), low);
+#pragma unroll
+        for (int c = 0; c < 32; c += 16) tmem_ld_x16(tmem + trow + (uint32_t)(32 * b + c), *reinterpret_cast<uint32_t(*)[16]>(&acc[c]));
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            v[i] = __uint_as_float(acc[kDigits * i + kDigits - 1]);
+#pragma unroll
+            for (int q = kDigits - 2; q >= 0; q--) v[i] = fmaf(v[i], 0.125f, __uint_as_float(acc[kDigits * i + q]));
+            v[i] = fmaf(v[i] * S_W, bars.e[imin(4 * b + i, nm - 1)], split == 0 ? __uint_as_float(low[i]) : 0.f);
+        }
+    };
+    // Y of the thread's output channel for the row m of the pass and the row m + step where `two` is set
+    auto finish = [&](int m, int step, bool two, float y0, float y1) {
+        y0 += bv, y1 += bv;
         if (p.gelu) f2_unpack(gelu_erf2(f2_pack(y0, y1)), y0, y1);
-        uint16_t* dst = p.y + (long long)(m0 + m) * p.y_stride + o;
+        uint16_t* dst = p.y + (long long)(m0 + m) * p.y_stride + o0 + row;
         dst[0] = f32_to_bf16_rn(y0);
-        if (m + 1 < nm) dst[p.y_stride] = f32_to_bf16_rn(y1);
+        if (two) dst[(long long)step * p.y_stride] = f32_to_bf16_rn(y1);
     };
     if (splits == 1) {
         if (warp >= 4 && done && ok) {
-            const float bv = bias ? bias[o0 + row] : 0.f;
-            for (int c = 16 * group; c < nm; c += 32) {
-                uint32_t acc[16];
-                tmem_ld_x16(tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)c, acc);
-                tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 16; j += 2)
-                    if (c + j < nm) finish(c + j, o0 + row, __uint_as_float(acc[j]), __uint_as_float(acc[j + 1]), bv);
+            for (int b = group; 4 * b < nm; b += 2) {
+                float v[4];
+                parts_of(b, v);
+                finish(4 * b, 1, 4 * b + 1 < nm, v[0], v[1]);
+                if (4 * b + 2 < nm) finish(4 * b + 2, 1, 4 * b + 3 < nm, v[2], v[3]);
             }
         }
     } else {
-        // The parts of a tile: CTA r of the cluster sums, in rank order, the row pairs j with j % splits = r.
+        // The parts of a tile: the CTA of part r sums, in the order of the parts, the rows m with m % splits = r.
         // The buffer takes the operand ring's place, so every CTA of the cluster is past its MMAs first.
         __syncwarp();
         cluster_sync();
-        float2* red = (float2*)sm;   // [source CTA][row pair / splits][128 output channels]
-        const int pairs = (nm + 1) / 2, own = (pairs + splits - 1) / splits;
+        float* red = (float*)sm;   // [part][row / splits][128 output channels]
+        const int per = (nm + splits - 1) / splits;
         if (warp >= 4 && done) {
-            for (int c = 16 * group; c < nm; c += 32) {
-                uint32_t acc[16];
-                tmem_ld_x16(tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)c, acc);
-                tmem_ld_wait();
+            for (int b = group; 4 * b < nm; b += 2) {
+                float v[4];
+                parts_of(b, v);
+                int dst = (4 * b) % splits, at = (4 * b) / splits;
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const int pr = c / 2 + j;
-                    if (pr < pairs) {
-                        const uint32_t at = mapa_shared(smem_u32(&red[(split * own + pr / splits) * 128 + row]), pr % splits);
-                        st_dsmem_f32(at, __uint_as_float(acc[2 * j]));
-                        st_dsmem_f32(at + 4, __uint_as_float(acc[2 * j + 1]));
-                    }
+                for (int i = 0; i < 4; i++) {
+                    if (4 * b + i < nm)
+                        st_dsmem_f32(mapa_shared(smem_u32(&red[(split * per + at) * 128 + row]), (uint32_t)dst), v[i]);
+                    if (++dst == splits) dst = 0, at++;
                 }
             }
         }
         __syncwarp();
         cluster_sync();
         if (warp >= 4 && done && ok) {
-            const int r = (tid - 128) & 127;
-            const float bv = bias ? bias[o0 + r] : 0.f;
-            for (int i = (tid - 128) >> 7; i * splits + split < pairs; i += 2) {
-                float a = 0.f, b = 0.f;
+            const int mine = split < nm ? (nm - split + splits - 1) / splits : 0;   // rows split, split + splits, ...
+            for (int n = 2 * group; n < mine; n += 4) {
+                float v0 = 0.f, v1 = 0.f;
                 for (int q = 0; q < splits; q++) {
-                    const float2 v = red[(q * own + i) * 128 + r];
-                    a += v.x, b += v.y;
+                    v0 += red[(q * per + n) * 128 + row];
+                    if (n + 1 < mine) v1 += red[(q * per + n + 1) * 128 + row];
                 }
-                finish(2 * (i * splits + split), o0 + r, a, b, bv);
+                finish(split + n * splits, splits, n + 1 < mine, v0, v1);
             }
         }
     }
@@ -347,51 +723,147 @@ __global__ void __launch_bounds__(kMainThreads, 2)
     }
 }
 
+// ------------------------------------------------------------------ host
+
+// Runs `set` (a kernel's attributes) on the first call for that kernel on the current device.  Concurrent
+// first calls may both run it; they set the same values.
+template <typename Set>
+cudaError_t once_per_device(const void* kernel, Set set) {
+    constexpr int kKernels = 8, kDevices = 64;
+    static std::atomic<const void*> names[kKernels];
+    static std::atomic<uint64_t> done[kKernels];   // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int i = 0;
+    for (; i < kKernels; i++) {
+        const void* at = names[i].load(std::memory_order_acquire);
+        if (at == nullptr && !names[i].compare_exchange_strong(at, kernel)) at = names[i].load(std::memory_order_acquire);
+        if (at == nullptr || at == kernel) break;
+    }
+    if (i == kKernels || dev >= kDevices) return set();
+    if (done[i].load(std::memory_order_acquire) >> dev & 1) return cudaSuccess;
+    if ((e = set()) == cudaSuccess) done[i].fetch_or(1ull << dev, std::memory_order_release);
+    return e;
+}
+
+// A call's two kernels; the product reads rows itself only when it writes their digits.
+template <typename F>
+auto by_format(int x_format, bool own, F f) {
+    if (x_format == DQ_ROWS_BF16)
+        return own ? f(k_rows_prepare<DQ_ROWS_BF16>, k_rows_product<DQ_ROWS_BF16, true>)
+                   : f(k_rows_prepare<DQ_ROWS_BF16>, k_rows_product<0, false>);
+    if (x_format == DQ_ROWS_E4M3)
+        return own ? f(k_rows_prepare<DQ_ROWS_E4M3>, k_rows_product<DQ_ROWS_E4M3, true>)
+                   : f(k_rows_prepare<DQ_ROWS_E4M3>, k_rows_product<0, false>);
+    return own ? f(k_rows_prepare<DQ_ROWS_E4M3_GROUP64>, k_rows_product<DQ_ROWS_E4M3_GROUP64, true>)
+               : f(k_rows_prepare<DQ_ROWS_E4M3_GROUP64>, k_rows_product<0, false>);
+}
+
+template <typename K>
+cudaError_t allow_smem(K kernel) {
+    return once_per_device((const void*)kernel, [=] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    });
+}
+
+// Clusters of `size` CTAs of the product, one CTA per SM, that fit on the current device at once (the same for all
+// forms), asked once per device and size.
+cudaError_t resident_clusters(int size, int* clusters) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][9];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= kDevices) return cudaErrorInvalidDevice;
+    std::atomic<int>& k = known[dev][size];
+    if ((*clusters = k.load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    auto kernel = k_rows_product<0, false>;
+    if ((e = allow_smem(kernel)) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)size;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)size, 1024);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kMaxSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaOccupancyMaxActiveClusters(clusters, kernel, &cfg)) != cudaSuccess) return e;
+    k.store(*clusters, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
 }  // namespace
 
 // How the product of `rows` rows is cut (RowsParams' fields from n_rows on).
-void rows_plan(RowsParams& p) {
-    // up to 256 rows of X a pass, evened out
-    const int passes = (int)cdiv(p.rows, 256);
-    p.n_rows = (int)cdiv(p.rows, passes);
-    p.n_pad = (int)cdiv(p.n_rows, 16) * 16;
+cudaError_t rows_plan(RowsParams& p) {
+    p.passes = (int)cdiv(p.rows, kPassRows);
+    p.n_rows = (int)cdiv(p.rows, p.passes);
     p.passes = (int)cdiv(p.rows, p.n_rows);
-    const bool small = p.n_pad <= 64;   // two CTAs per SM: 256 tensor-memory columns and 113 KB each
-    p.tmem_cols = small ? 256 : 512;
-    p.d_cols = small ? 64 : 256;
-    p.ring = small ? 6 : 8;
-    const int slot = p.n_pad * 128, room = small ? 110 * 1024 : kMaxSmem - 1024;
-    p.stages_b = small ? (p.n_pad <= 16 ? 8 : p.n_pad <= 32 ? 6 : 4) : (p.n_pad <= 128 ? 6 : 4);
-    p.stages_a = imin(kRowsStages, (room - p.stages_b * slot) / (int)kRowsStageA);
-    p.smem = p.stages_a * (int)kRowsStageA + p.stages_b * slot + 1024;
-    // as many parts of the channels as still let every CTA be resident at once
-    const int tiles = p.Co / 128 * p.passes, places = small ? 296 : 148;
-    p.splits = 1;
-    while (p.splits < 8 && tiles * p.splits * 2 <= places && p.splits * 2 <= p.Ci / 256) p.splits *= 2;
+    p.n_pad = p.n_rows * kDigits;
+    p.d_cols = (int)cdiv(p.n_pad, 32) * 32;
+    const int tiles = p.Co / 128, k256 = p.Ci / 256, digits = p.n_pad * 128;
+    // Up to kOwnRows rows two CTAs share an SM (256 tensor-memory columns each) and write their digits
+    // themselves, if those and a ring of enough stages fit on half an SM, or else on a whole one.
+    for (int attempt = p.rows <= kOwnRows ? 0 : 2; attempt < 3; attempt++) {
+        const bool own = attempt < 2, small = attempt == 0;
+        // a cluster splits the channels as far as every CTA is still resident at once
+        p.splits = 1;
+        const int tries[] = {8, 6, 4, 3, 2};
+        for (int s : tries) {
+            int clusters = 0;
+            if (s > k256) continue;
+            cudaError_t e = resident_clusters(s, &clusters);
+            if (e != cudaSuccess) return e;
+            if (tiles * p.passes <= clusters * (small ? 2 : 1)) {
+                p.splits = s;
+                break;
+            }
+        }
+        const int nA = (int)cdiv(k256, p.splits);
+        p.own_digits = own;
+        p.tmem_cols = small ? 256 : 512;
+        p.smem = small ? kSmallSmem : kMaxSmem;
+        const int room = p.smem - 1024 - (own ? nA * digits : 0);
+        const int stage = (int)(kCodeBytes + kScaleBytes) + (own ? 0 : digits);
+        p.stages = room < 0 ? 0 : imin(imin(kStages, room / stage), (p.tmem_cols - p.d_cols - (int)cdiv(p.n_rows, 16) * 16 - 8) / 16);
+        if (own && (p.stages < imin(small ? 4 : 6, nA) || nA > kOwnTurns * own_warps(p.rows))) continue;
+        break;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t launch_rows(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const CUtensorMap& tm_x, const CUtensorMap& tm_l2,
                         const CUtensorMap& tm_u, const RowsParams& p, cudaStream_t st) {
-    cudaError_t e = launch_rows_prepare(p, false, st);
-    if (e != cudaSuccess) return e;
-    e = once_per_device((const void*)k_rows_main, [] {
-        return cudaFuncSetAttribute(k_rows_main, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    return by_format(p.x_format, p.own_digits != 0, [&](auto prepare, auto product) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = kPrepCluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.stream = st;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        const long long blocks = p.own_digits ? 0 : cdiv((long long)p.rows * cdiv(p.Ci, kBlockChannels), kPrepCluster);
+        cfg.gridDim = dim3((unsigned)((blocks + cdiv(p.rows, 16) * cdiv(p.rank, 32)) * kPrepCluster));
+        cfg.blockDim = dim3(kPrepThreads);
+        // the product's split of the SM between L1 and shared memory: a different one would keep its CTAs off an
+        // SM until this kernel's have left
+        cudaError_t e = once_per_device((const void*)prepare, [&] {
+            return cudaFuncSetAttribute(prepare, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        });
+        if (e != cudaSuccess || (e = cudaLaunchKernelEx(&cfg, prepare, p)) != cudaSuccess) return e;
+        if ((e = allow_smem(product)) != cudaSuccess) return e;
+        attr[1].val.clusterDim.x = (unsigned)p.splits;
+        cfg.gridDim = dim3((unsigned)p.splits, (unsigned)(p.Co / 128), (unsigned)p.passes);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = (size_t)p.smem;
+        return cudaLaunchKernelEx(&cfg, product, tm_w, tm_s, tm_x, tm_l2, tm_u, p);
     });
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)p.splits;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)p.splits, (unsigned)(p.Co / 128), (unsigned)p.passes);
-    cfg.blockDim = dim3(kMainThreads);
-    cfg.dynamicSmemBytes = (size_t)p.smem;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_rows_main, tm_w, tm_s, tm_x, tm_l2, tm_u, p);
 }
 
 }  // namespace dq
