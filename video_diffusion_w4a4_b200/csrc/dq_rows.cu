@@ -265,9 +265,9 @@ __device__ __forceinline__ void load_rows_16(const RowsParams& p, int m0, int nm
     }
 }
 
-constexpr int kPrepThreads = 512, kPrepCluster = 8, kBlockChannels = 8 * kPrepThreads;
+constexpr int kPrepThreads = 1024, kPrepCluster = 8, kBlockChannels = 8 * kPrepThreads;
 
-// Digits of 4096 channels of a row.  Each block finds the row's largest magnitude for itself: a second read of at
+// Digits of 8192 channels of a row.  Each block finds the row's largest magnitude for itself: a second read of at
 // most 28 KB, from L2, costs less than a hand-off between blocks.
 template <int kFmt>
 __device__ __forceinline__ void digits_block(const RowsParams& p, int m, int part) {
@@ -299,41 +299,47 @@ __device__ __forceinline__ void digits_block(const RowsParams& p, int m, int par
 }
 
 // U = xv L1 of 16 rows and 32 ranks by a cluster of eight CTAs, an eighth of the channels each: a warp takes 16 of
-// the ranks and every eighth 64-channel block, lane t of a quad 16 channels of a block (any assignment of channels
+// the ranks and every sixteenth 64-channel block, lane t of a quad 16 channels of a block (any assignment of channels
 // to the MMA's k is right that both operands share).  The sums are joined in rank order through distributed
 // shared memory and kept as BF16 hi + lo, 2^-17 of the value.
 template <int kFmt, bool kHalf>
-__device__ __forceinline__ void lowrank_cluster(const RowsParams& p, int index) {
-    __shared__ float wpart[8][16][32], part[16][32];
+__device__ __forceinline__ void lowrank_cluster(const RowsParams& p, int index, float (*wpart)[16][32], float (*part)[32]) {
+    constexpr int kAhead = kHalf ? 2 : 1;   // blocks loaded ahead, as registers allow
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int crank = (int)cluster_ctarank(), rgroups = (p.rank + 31) / 32;
     const int m0 = index / rgroups * 16, nm = imin(16, p.rows - m0), j0 = index % rgroups * 32;
     const int nblk = p.Ci / 64, b0 = nblk * crank / kPrepCluster, b1 = nblk * (crank + 1) / kPrepCluster;
     const int jw = j0 + 16 * (warp & 1), ks = warp >> 1;
-    if (p.own_digits) {
-        // L1's part for this CTA on its way before the product is let in
-        for (int j = j0 + warp; j < imin(j0 + 32, p.rank); j += kPrepThreads / 32)
-            for (int b = b0 + lane; b < b1; b += 32)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.l1 + (long long)j * p.Ci + b * 64));
-        griddep_launch();
-    }
     float acc[2][4] = {};
-    if (jw < p.rank) {
-#pragma unroll 2
-        for (int b = b0 + ks; b < b1; b += 8) {
-            uint32_t xa[2][8];
-            float sc[2];
-            load_rows_16<kFmt, kHalf>(p, m0, nm, b, g, t, xa, sc);
+    for (int b = b0 + ks, first = 1; first || b < b1; b += 16 * kAhead, first = 0) {
+        uint32_t xa[kAhead][2][8];
+        float sc[kAhead][2];
+        uint4 l1[kAhead][2][2];
+#pragma unroll
+        for (int h = 0; h < kAhead; h++) {
+            const int bb = b + 16 * h;
+            const bool in = bb < b1 && jw < p.rank;
+            load_rows_16<kFmt, kHalf>(p, m0, in ? nm : 0, bb, g, t, xa[h], sc[h]);
 #pragma unroll
             for (int n = 0; n < 2; n++) {
-                const uint4* src = reinterpret_cast<const uint4*>(p.l1 + (long long)(jw + 8 * n + g) * p.Ci + b * 64 + t * 16);
-                const uint4 u = src[0], v = src[1];
+                const uint4* src = reinterpret_cast<const uint4*>(p.l1 + (long long)(jw + 8 * n + g) * p.Ci + bb * 64 + t * 16);
+                l1[h][n][0] = in ? src[0] : make_uint4(0, 0, 0, 0);
+                l1[h][n][1] = in ? src[1] : make_uint4(0, 0, 0, 0);
+            }
+        }
+        // up to 16384 channels of at most eight rows all loads are under way by now
+        if (kHalf && first) griddep_launch();
+#pragma unroll
+        for (int h = 0; h < kAhead; h++) {
+#pragma unroll
+            for (int n = 0; n < 2; n++) {
+                const uint4 u = l1[h][n][0], v = l1[h][n][1];
                 float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_16816(d, xa[0][0], xa[1][0], xa[0][1], xa[1][1], u.x, u.y);
-                mma_16816(d, xa[0][2], xa[1][2], xa[0][3], xa[1][3], u.z, u.w);
-                mma_16816(d, xa[0][4], xa[1][4], xa[0][5], xa[1][5], v.x, v.y);
-                mma_16816(d, xa[0][6], xa[1][6], xa[0][7], xa[1][7], v.z, v.w);
-                const float s0 = kFmt == DQ_ROWS_E4M3_GROUP64 ? sc[0] : 1.f, s1 = kFmt == DQ_ROWS_E4M3_GROUP64 ? sc[1] : 1.f;
+                mma_16816(d, xa[h][0][0], xa[h][1][0], xa[h][0][1], xa[h][1][1], u.x, u.y);
+                mma_16816(d, xa[h][0][2], xa[h][1][2], xa[h][0][3], xa[h][1][3], u.z, u.w);
+                mma_16816(d, xa[h][0][4], xa[h][1][4], xa[h][0][5], xa[h][1][5], v.x, v.y);
+                mma_16816(d, xa[h][0][6], xa[h][1][6], xa[h][0][7], xa[h][1][7], v.z, v.w);
+                const float s0 = kFmt == DQ_ROWS_E4M3_GROUP64 ? sc[h][0] : 1.f, s1 = kFmt == DQ_ROWS_E4M3_GROUP64 ? sc[h][1] : 1.f;
                 acc[n][0] = fmaf(d[0], s0, acc[n][0]);
                 acc[n][1] = fmaf(d[1], s0, acc[n][1]);
                 acc[n][2] = fmaf(d[2], s1, acc[n][2]);
@@ -341,6 +347,7 @@ __device__ __forceinline__ void lowrank_cluster(const RowsParams& p, int index) 
             }
         }
     }
+    if (!kHalf) griddep_launch();
     // lane (g, t): rows g and g + 8, ranks 8 n + 2 t and the next of the warp's sixteen
 #pragma unroll
     for (int n = 0; n < 2; n++) {
@@ -349,11 +356,10 @@ __device__ __forceinline__ void lowrank_cluster(const RowsParams& p, int index) 
         w0[8 * 32] = acc[n][2], w0[8 * 32 + 1] = acc[n][3];
     }
     __syncthreads();
-    if (!p.own_digits) griddep_launch();   // the CTA's loads have arrived
-    {
+    if (warp < 16) {
         float u = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; k++) u += wpart[k][warp][lane];
+        for (int k = 0; k < 16; k++) u += wpart[k][warp][lane];
         part[warp][lane] = u;
     }
     cluster_sync();
@@ -380,15 +386,18 @@ __device__ __forceinline__ void lowrank_cluster(const RowsParams& p, int index) 
 template <int kFmt>
 __global__ void __launch_bounds__(kPrepThreads) k_rows_prepare(RowsParams p) {
     griddep_wait();     // the launch before this one may still read the workspace, or write X
-    const int parts = (p.Ci + kBlockChannels - 1) / kBlockChannels, blocks = p.own_digits ? 0 : p.rows * parts;
-    const int first = (blocks + kPrepCluster - 1) / kPrepCluster * kPrepCluster, b = (int)blockIdx.x;
-    if (b == first && threadIdx.x == 0) *p.status = header_ok(p) ? 0 : kStatusBadWeight;
-    if (b < blocks)
-        digits_block<kFmt>(p, b / parts, b % parts);
-    else if (b >= first && p.rows <= 8)
-        lowrank_cluster<kFmt, true>(p, (b - first) / kPrepCluster);
-    else if (b >= first)
-        lowrank_cluster<kFmt, false>(p, (b - first) / kPrepCluster);
+    __shared__ float wpart[16][16][32], part[16][32];
+    // the low-rank clusters first: they take longest
+    const int parts = (p.Ci + kBlockChannels - 1) / kBlockChannels, b = (int)blockIdx.x;
+    const int low = (p.rows + 15) / 16 * ((p.rank + 31) / 32) * kPrepCluster;
+    if (b == 0 && threadIdx.x == 0) *p.status = header_ok(p) ? 0 : kStatusBadWeight;
+    if (b >= low) {
+        if (b - low < p.rows * parts) digits_block<kFmt>(p, (b - low) / parts, (b - low) % parts);
+    } else if (p.rows <= 8) {
+        lowrank_cluster<kFmt, true>(p, b / kPrepCluster, wpart, part);
+    } else {
+        lowrank_cluster<kFmt, false>(p, b / kPrepCluster, wpart, part);
+    }
 }
 
 // ------------------------------------------------------------------ the product
@@ -421,16 +430,22 @@ struct Bars {
 __host__ __device__ constexpr int own_warps(int rows) { return rows == 1 ? 8 : rows == 2 ? 4 : rows <= 4 ? 2 : 1; }
 
 template <int kFmt>
-__device__ __forceinline__ void write_own_digits(const RowsParams& p, Bars& bars, uint8_t* dst, int c0, int channels) {
+__device__ __forceinline__ void load_own_rows(const RowsParams& p, int c0, int channels, Raw8<kFmt> (&raw)[kOwnTurns]) {
     const int ew = (int)(threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
     const int per = own_warps(p.rows), m = ew / per, part = ew % per, first = (part * 32 + lane) * 8;
-    Raw8<kFmt> raw[kOwnTurns];
-    float am = 0.f;
 #pragma unroll
     for (int i = 0; i < kOwnTurns; i++) {
         raw[i] = {};
         if (m < p.rows && first + i * per * 256 < channels) raw[i] = load_raw8<kFmt>(p, m, c0 + first + i * per * 256);
     }
+}
+
+template <int kFmt>
+__device__ __forceinline__ void write_own_digits(const RowsParams& p, Bars& bars, uint8_t* dst, int channels,
+                                                 const Raw8<kFmt> (&raw)[kOwnTurns]) {
+    const int ew = (int)(threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
+    const int per = own_warps(p.rows), m = ew / per, part = ew % per, first = (part * 32 + lane) * 8;
+    float am = 0.f;
 #pragma unroll
     for (int i = 0; i < kOwnTurns; i++) am = max_nan(am, amax8<kFmt>(raw[i]));
 #pragma unroll
@@ -489,6 +504,9 @@ __global__ void __launch_bounds__(kThreads, kOwn ? 2 : 1)
     const uint32_t n16 = (uint32_t)(p.n_rows + 15) & ~15u;
     volatile int* abort_flag = &bars.abort_flag;
 
+    // the rows whose digits this CTA writes, before the weight's loads
+    Raw8<kFmt> raw[kOwnTurns];
+    if (own && warp >= 4) load_own_rows<kFmt>(p, a0 * 256, nA * 256, raw);
     if (tid == 0) {
         for (int s = 0; s < S; s++) {
             mbar_init(&bars.full[s], own ? 1 : 2);   // one producer, or both
@@ -636,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, kOwn ? 2 : 1)
             asm volatile("bar.arrive 2, 160;" ::: "memory");
         }
         if (own) {
-            write_own_digits<kFmt>(p, bars, digits, a0 * 256, nA * 256);
+            write_own_digits<kFmt>(p, bars, digits, nA * 256, raw);
         } else {
             griddep_wait();   // the rows' factors come from k_rows_prepare
             if (et < nm) bars.e[et] = p.e[m0 + et];
