@@ -922,13 +922,15 @@ int dq_rows_forward(const void* X, int x_format, long long x_stride, const float
     if (!map_2d(&tm_w, p.packed_w + pl.off_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Ci / 2, Co, 128, 128))
         return map_fail("weight codes");
     if (!map_sfb_lanes(&tm_s, p.packed_w + pl.off_scales, Ci, Co)) return map_fail("weight scales");
-    if (p.own_digits)
-        tm_x = tm_w;   // not read
-    else if (!map_2d(&tm_x, p.digits, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Ci / 2, (uint64_t)rows * 8, 128, p.n_pad))
-        return map_fail("digits");
-    if (!map_2d(&tm_l2, L2_slab, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pl.slab, Co, 64, 128)) return map_fail("L2");
-    if (!map_2d(&tm_u, p.u, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pl.slab, rows, 64, (uint32_t)dq::cdiv(p.n_rows, 16) * 16))
-        return map_fail("U");
+    if (p.own_digits) {
+        tm_x = tm_l2 = tm_u = tm_w;   // not read
+    } else {
+        if (!map_2d(&tm_x, p.digits, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Ci / 2, (uint64_t)rows * 8, 128, p.n_pad))
+            return map_fail("digits");
+        if (!map_2d(&tm_l2, L2_slab, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pl.slab, Co, 64, 128)) return map_fail("L2");
+        if (!map_2d(&tm_u, p.u, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pl.slab, rows, 64, (uint32_t)dq::cdiv(p.n_rows, 16) * 16))
+            return map_fail("U");
+    }
     e = dq::launch_rows(tm_w, tm_s, tm_x, tm_l2, tm_u, p, (cudaStream_t)stream);
     return e == cudaSuccess ? DQ_OK : cuda_fail(e, "few-row product");
 }

@@ -139,9 +139,10 @@ struct RowsParams {
     uint64_t budget_ns;
     // the cut of the product (rows_plan)
     int n_rows, n_pad, passes;  // rows of X per pass, their digits' columns
-    int splits;                 // parts of the channels: the CTAs of a cluster
-    int stages, smem, tmem_cols, d_cols;
-    int own_digits;             // the product writes the digits itself
+    int splits, group;          // parts of the channels, and tiles, of a cluster
+    int stages, d_cols;
+    int own_digits, own_stages; // the product writes the digits itself (of up to so many 256-channel stages), and U L2
+    int u_parts;                //   parts of a CTA's channels of U
 };
 cudaError_t rows_plan(RowsParams& p);
 cudaError_t launch_rows(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const CUtensorMap& tm_x,

@@ -14,22 +14,27 @@
 // The low-rank factor is BF16 K steps of the same warp into columns of their own
 // (U = xv L1 as hi + lo, times L2).
 //
-//   k_rows_prepare   U, and digits and unit 2^(e-1) of each row (more than kOwnRows
-//                    rows; fewer are left to the product)
 //   k_rows_product   128 output channels (the MMA's M) times up to 32 rows (256
 //                    columns) per CTA.  One warp keeps codes and scales in flight,
 //                    one the digits, one issues scale copies and MMAs, eight write
-//                    the output (and before it, for the fewest rows, the digits).
-//                    When the tiles alone do not fill the GPU a cluster splits the
-//                    channels and sums its parts in order through distributed
-//                    shared memory.
+//                    the output.  When the tiles alone do not fill the GPU a cluster
+//                    splits the channels and sums its parts in order through
+//                    distributed shared memory.
+//   k_rows_prepare   what it needs of the rows: digits and unit 2^(e-1), and U = xv
+//                    L1, which the product multiplies with L2 as BF16 K steps (hi +
+//                    lo) into columns of their own.
 //
-// k_rows_product is launched while k_rows_prepare runs (programmatic launch): its
-// loads of the weight need only what was there before both.  Once they stream,
-// a load of anything else waits behind them for 2 to 4 us, a ring of the weight's
-// stages per SM deep; so the few other loads come first, or where nothing waits for
-// them, and k_rows_prepare lets the product in when its own have arrived, unless
-// only U is left to it, which the product needs last.
+// Up to kOwnRows rows k_rows_product does all of it (one launch): the warps that
+// write the output write the digits of the CTA's channels before it, and eight more
+// form the low-rank term beside the product.  The CTAs of a cluster, parts of tiles
+// and whole ones, take a share of the channels of U each and exchange their sums
+// through distributed shared memory, so that L1 is read once a cluster.
+//
+// Once the weight streams, a load of anything else waits behind it for 2 to 4 us, a
+// ring of the weight's stages per SM deep.  So the other loads come first, or where
+// nothing waits for them: k_rows_product holds the stream back until they are under
+// way, and k_rows_prepare lets the product in when its own have arrived
+// (programmatic launch).
 #include "../../include/deltaquant.h"
 #include "dq_common.h"
 #include "dq_internal.h"
@@ -44,20 +49,50 @@ namespace {
 constexpr int kDigits = 8;                       // FP4 digits of a value
 constexpr int kPassRows = 32;                    // rows of X per CTA: 256 MMA columns
 constexpr int kOwnRows = 8;                      // up to so many rows the product writes the digits itself
-constexpr int kOwnTurns = 8;                     // pieces of eight channels a thread holds for that
-constexpr int kThreads = 384;                    // producers of A and B, MMA, a spare warp, eight epilogue warps
+constexpr int kOwnTurns = 10;                    // pieces of eight channels a thread holds for that
+// producers of A and B, MMA, a spare warp, eight epilogue warps; eight for the low-rank term
+constexpr int product_threads(bool own) { return own ? 640 : 384; }
 constexpr int kEpiThreads = 256;
 constexpr int kStages = 16;                      // stages of the operand ring at most
 constexpr uint32_t kCodeBytes = 128 * 128;       // codes of 128 output channels x 256 input channels
 constexpr uint32_t kScaleBytes = 4 * 512;        // their group scales
-// Dynamic shared memory of a CTA that has an SM to itself, and of one of two that share it (a third
-// never fits, so none waits on an SM for tensor memory while its cluster waits for it).
-constexpr int kMaxSmem = 225 * 1024, kSmallSmem = 111 * 1024;
+// Dynamic shared memory: a CTA has an SM to itself (so that none waits there for tensor memory while its cluster
+// waits for it), and all of the tensor memory.
+constexpr int kSmem = 224 * 1024;
+constexpr uint32_t kTmemCols = 512;
 
 // ------------------------------------------------------------------ small pieces
 
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void bar_arrive(int id, int nthreads) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// As mbar_wait, for a barrier that other CTAs of the cluster arrive on: acquires what they wrote before.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                                  uint64_t budget_ns) {
+    const uint64_t t0 = globaltimer();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (globaltimer() - t0 > budget_ns) {
+            *abort_flag = 1;
+            atomicCAS(status, 0, kStatusTimeout);
+            return false;
+        }
+    }
+}
 
 // D(16 x 8) += A(16 x 16) B(16 x 8), BF16 operands, fp32 sums
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -298,64 +333,78 @@ __device__ __forceinline__ void digits_block(const RowsParams& p, int m, int par
     for (int q = 0; q < kDigits; q++) *reinterpret_cast<uint32_t*>(dst + (size_t)q * (p.Ci / 2)) = next_digits8(v2);
 }
 
-// U = xv L1 of 16 rows and 32 ranks by a cluster of eight CTAs, an eighth of the channels each: a warp takes 16 of
-// the ranks and every sixteenth 64-channel block, lane t of a quad 16 channels of a block (any assignment of channels
-// to the MMA's k is right that both operands share).  The sums are joined in rank order through distributed
-// shared memory and kept as BF16 hi + lo, 2^-17 of the value.
+// acc[n] += X L1 over the 64 channels of block b for 16 rows (or eight) and the ranks j0 + 8 n to + 7: lane t of a
+// quad has 16 of the channels (any assignment of channels to the MMA's k is right that both operands share).  The
+// loads are a call of their own, so that several blocks' can be under way.
+template <bool kHalf>
+struct LowRankBlock {
+    uint32_t x[2][8];
+    float s[2];
+    uint4 l1[2][2];
+};
+
 template <int kFmt, bool kHalf>
+__device__ __forceinline__ void lowrank_load(const RowsParams& p, int m0, int nm, int j0, int b, bool in, int g, int t,
+                                             LowRankBlock<kHalf>& q) {
+    load_rows_16<kFmt, kHalf>(p, m0, in ? nm : 0, b, g, t, q.x, q.s);
+#pragma unroll
+    for (int n = 0; n < 2; n++) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.l1 + (long long)(j0 + 8 * n + g) * p.Ci + b * 64 + t * 16);
+        q.l1[n][0] = in ? src[0] : make_uint4(0, 0, 0, 0);
+        q.l1[n][1] = in ? src[1] : make_uint4(0, 0, 0, 0);
+    }
+}
+
+template <int kFmt, bool kHalf>
+__device__ __forceinline__ void lowrank_add(const LowRankBlock<kHalf>& q, float (&acc)[2][4]) {
+#pragma unroll
+    for (int n = 0; n < 2; n++) {
+        const uint4 u = q.l1[n][0], v = q.l1[n][1];
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_16816(d, q.x[0][0], q.x[1][0], q.x[0][1], q.x[1][1], u.x, u.y);
+        mma_16816(d, q.x[0][2], q.x[1][2], q.x[0][3], q.x[1][3], u.z, u.w);
+        mma_16816(d, q.x[0][4], q.x[1][4], q.x[0][5], q.x[1][5], v.x, v.y);
+        mma_16816(d, q.x[0][6], q.x[1][6], q.x[0][7], q.x[1][7], v.z, v.w);
+        const float s0 = kFmt == DQ_ROWS_E4M3_GROUP64 ? q.s[0] : 1.f, s1 = kFmt == DQ_ROWS_E4M3_GROUP64 ? q.s[1] : 1.f;
+        acc[n][0] = fmaf(d[0], s0, acc[n][0]);
+        acc[n][1] = fmaf(d[1], s0, acc[n][1]);
+        acc[n][2] = fmaf(d[2], s1, acc[n][2]);
+        acc[n][3] = fmaf(d[3], s1, acc[n][3]);
+    }
+}
+
+// Lane (g, t) holds the rows g and g + 8 and the ranks 8 n + 2 t and the next: into a row-major array of `rank` columns
+template <bool kHalf>
+__device__ __forceinline__ void lowrank_store(float* dst, int rank, int g, int t, const float (&acc)[2][4]) {
+#pragma unroll
+    for (int n = 0; n < 2; n++) {
+        float* o = dst + g * rank + 8 * n + 2 * t;
+        o[0] = acc[n][0], o[1] = acc[n][1];
+        if (!kHalf) o[8 * rank] = acc[n][2], o[8 * rank + 1] = acc[n][3];
+    }
+}
+
+// U of 16 rows and 32 ranks by a cluster of eight CTAs, an eighth of the channels each: a warp takes 16 of the ranks
+// and every sixteenth 64-channel block.  The sums are joined in rank order through distributed shared memory and
+// kept as BF16 hi + lo, 2^-17 of the value.
+template <int kFmt>
 __device__ __forceinline__ void lowrank_cluster(const RowsParams& p, int index, float (*wpart)[16][32], float (*part)[32]) {
-    constexpr int kAhead = kHalf ? 2 : 1;   // blocks loaded ahead, as registers allow
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int crank = (int)cluster_ctarank(), rgroups = (p.rank + 31) / 32;
     const int m0 = index / rgroups * 16, nm = imin(16, p.rows - m0), j0 = index % rgroups * 32;
     const int nblk = p.Ci / 64, b0 = nblk * crank / kPrepCluster, b1 = nblk * (crank + 1) / kPrepCluster;
     const int jw = j0 + 16 * (warp & 1), ks = warp >> 1;
     float acc[2][4] = {};
-    for (int b = b0 + ks, first = 1; first || b < b1; b += 16 * kAhead, first = 0) {
-        uint32_t xa[kAhead][2][8];
-        float sc[kAhead][2];
-        uint4 l1[kAhead][2][2];
-#pragma unroll
-        for (int h = 0; h < kAhead; h++) {
-            const int bb = b + 16 * h;
-            const bool in = bb < b1 && jw < p.rank;
-            load_rows_16<kFmt, kHalf>(p, m0, in ? nm : 0, bb, g, t, xa[h], sc[h]);
-#pragma unroll
-            for (int n = 0; n < 2; n++) {
-                const uint4* src = reinterpret_cast<const uint4*>(p.l1 + (long long)(jw + 8 * n + g) * p.Ci + bb * 64 + t * 16);
-                l1[h][n][0] = in ? src[0] : make_uint4(0, 0, 0, 0);
-                l1[h][n][1] = in ? src[1] : make_uint4(0, 0, 0, 0);
-            }
-        }
-        // up to 16384 channels of at most eight rows all loads are under way by now
-        if (kHalf && first) griddep_launch();
-#pragma unroll
-        for (int h = 0; h < kAhead; h++) {
-#pragma unroll
-            for (int n = 0; n < 2; n++) {
-                const uint4 u = l1[h][n][0], v = l1[h][n][1];
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_16816(d, xa[h][0][0], xa[h][1][0], xa[h][0][1], xa[h][1][1], u.x, u.y);
-                mma_16816(d, xa[h][0][2], xa[h][1][2], xa[h][0][3], xa[h][1][3], u.z, u.w);
-                mma_16816(d, xa[h][0][4], xa[h][1][4], xa[h][0][5], xa[h][1][5], v.x, v.y);
-                mma_16816(d, xa[h][0][6], xa[h][1][6], xa[h][0][7], xa[h][1][7], v.z, v.w);
-                const float s0 = kFmt == DQ_ROWS_E4M3_GROUP64 ? sc[h][0] : 1.f, s1 = kFmt == DQ_ROWS_E4M3_GROUP64 ? sc[h][1] : 1.f;
-                acc[n][0] = fmaf(d[0], s0, acc[n][0]);
-                acc[n][1] = fmaf(d[1], s0, acc[n][1]);
-                acc[n][2] = fmaf(d[2], s1, acc[n][2]);
-                acc[n][3] = fmaf(d[3], s1, acc[n][3]);
-            }
+    if (jw < p.rank) {
+        for (int b = b0 + ks; b < b1; b += 16) {
+            LowRankBlock<false> q;
+            lowrank_load<kFmt, false>(p, m0, nm, jw, b, true, g, t, q);
+            lowrank_add<kFmt, false>(q, acc);
         }
     }
-    if (!kHalf) griddep_launch();
-    // lane (g, t): rows g and g + 8, ranks 8 n + 2 t and the next of the warp's sixteen
-#pragma unroll
-    for (int n = 0; n < 2; n++) {
-        float* w0 = &wpart[ks][g][16 * (warp & 1) + 8 * n + 2 * t];
-        w0[0] = acc[n][0], w0[1] = acc[n][1];
-        w0[8 * 32] = acc[n][2], w0[8 * 32 + 1] = acc[n][3];
-    }
+    lowrank_store<false>(&wpart[ks][0][16 * (warp & 1)], 32, g, t, acc);
     __syncthreads();
+    griddep_launch();   // the CTA's loads have arrived
     if (warp < 16) {
         float u = 0.f;
 #pragma unroll
@@ -391,13 +440,10 @@ __global__ void __launch_bounds__(kPrepThreads) k_rows_prepare(RowsParams p) {
     const int parts = (p.Ci + kBlockChannels - 1) / kBlockChannels, b = (int)blockIdx.x;
     const int low = (p.rows + 15) / 16 * ((p.rank + 31) / 32) * kPrepCluster;
     if (b == 0 && threadIdx.x == 0) *p.status = header_ok(p) ? 0 : kStatusBadWeight;
-    if (b >= low) {
-        if (b - low < p.rows * parts) digits_block<kFmt>(p, (b - low) / parts, (b - low) % parts);
-    } else if (p.rows <= 8) {
-        lowrank_cluster<kFmt, true>(p, b / kPrepCluster, wpart, part);
-    } else {
-        lowrank_cluster<kFmt, false>(p, b / kPrepCluster, wpart, part);
-    }
+    if (b < low)
+        lowrank_cluster<kFmt>(p, b / kPrepCluster, wpart, part);
+    else if (b - low < p.rows * parts)
+        digits_block<kFmt>(p, (b - low) / parts, (b - low) % parts);
 }
 
 // ------------------------------------------------------------------ the product
@@ -416,7 +462,7 @@ struct Ring {
 };
 
 struct Bars {
-    uint64_t full[kStages], empty[kStages], accf, digits[kOwnTurns];
+    uint64_t full[kStages], empty[kStages], accf, digits[kOwnTurns], u;
     float e[kPassRows];   // the rows' factors
     float amax[8];        // own digits: each warp's part of its row's largest magnitude
     uint32_t tmem;
@@ -481,8 +527,85 @@ __device__ __forceinline__ void write_own_digits(const RowsParams& p, Bars& bars
     }
 }
 
+// Low-rank term beside the product (at most kOwnRows rows): this CTA's share of the channels of U, cut further among
+// eight warps (16 ranks x every u_parts-th block of 64 channels), exchanged within the cluster, then U L2 for the
+// rows that this CTA finishes: low[i][output channel] of row split + i splits.
+template <int kFmt>
+__device__ __forceinline__ void lowrank_term(const RowsParams& p, Bars& bars, float* up, float* su, float* low, int o0,
+                                             int crank, int csize, int split, int splits) {
+    const int ut = (int)threadIdx.x - 384, uw = ut >> 5, lane = ut & 31, g = lane >> 2, t = lane & 3;
+    const int items = p.rank / 16, nblk = p.Ci / 64, b0 = nblk * crank / csize, b1 = nblk * (crank + 1) / csize;
+    const int row = ut & 127, mine = split < p.rows ? (p.rows - split + splits - 1) / splits : 0;
+    const uint4* l2 = reinterpret_cast<const uint4*>(p.l2 + (size_t)(o0 + row) * p.slab);
+    uint4 l2w[4];   // the first 32 ranks of this thread's output channel
+#pragma unroll
+    for (int j = 0; j < 4; j++) l2w[j] = 8 * j < p.rank ? l2[j] : make_uint4(0, 0, 0, 0);
+    bool first = true;
+    for (int w = uw; w < items * p.u_parts; w += 8) {
+        const int part = w / items, j0 = (w - part * items) * 16;
+        float acc[2][4] = {};
+        for (int b = b0 + part; first || b < b1; b += 2 * p.u_parts) {
+            LowRankBlock<true> q[2];
+#pragma unroll
+            for (int h = 0; h < 2; h++) lowrank_load<kFmt, true>(p, 0, p.rows, j0, b + h * p.u_parts, b + h * p.u_parts < b1, g, t, q[h]);
+            if (first) bar_arrive(3, 32 + 512);   // the weight may follow
+            first = false;
+#pragma unroll
+            for (int h = 0; h < 2; h++) lowrank_add<kFmt, true>(q[h], acc);
+        }
+        lowrank_store<true>(up + part * 8 * p.rank + j0, p.rank, g, t, acc);
+    }
+    if (first) bar_arrive(3, 32 + 512);
+    bar_sync(4, 256);
+    for (int e = ut; e < 8 * p.rank; e += 256) {
+        float s = up[e];
+        for (int k = 1; k < p.u_parts; k++) s += up[k * 8 * p.rank + e];
+        up[e] = s;
+    }
+    bar_sync(4, 256);
+    cluster_wait();
+    if (ut < csize) mbar_arrive_cluster(mapa_shared(smem_u32(&bars.u), (uint32_t)ut));
+    mbar_wait_cluster(&bars.u, 0, &bars.abort_flag, p.status, p.budget_ns);
+    for (int e = ut; e < p.rows * p.rank; e += 256) {
+        const uint32_t at = smem_u32(&up[e]);
+        float v[8], u = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; c++) v[c] = c < csize ? ld_dsmem_f32(mapa_shared(at, (uint32_t)c)) : 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; c++) u += v[c];
+        if (kFmt == DQ_ROWS_E4M3) u *= p.x_scales[e / p.rank];
+        su[e] = u;
+    }
+    bar_sync(4, 256);
+    for (int i = ut >> 7; i < mine; i += 2) {
+        const float* u = su + (split + i * splits) * p.rank;
+        float y = 0.f;
+        for (int j0 = 0; j0 < p.rank; j0 += 32) {
+            if (j0) {
+#pragma unroll
+                for (int j = 0; j < 4; j++) l2w[j] = j0 + 8 * j < p.rank ? l2[j0 / 8 + j] : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                if (j0 + 8 * j >= p.rank) break;
+                const float4 u0 = *reinterpret_cast<const float4*>(u + j0 + 8 * j), u1 = *reinterpret_cast<const float4*>(u + j0 + 8 * j + 4);
+                y = fmaf(u0.x, bf16_lo(l2w[j].x), y), y = fmaf(u0.y, bf16_hi(l2w[j].x), y);
+                y = fmaf(u0.z, bf16_lo(l2w[j].y), y), y = fmaf(u0.w, bf16_hi(l2w[j].y), y);
+                y = fmaf(u1.x, bf16_lo(l2w[j].z), y), y = fmaf(u1.y, bf16_hi(l2w[j].z), y);
+                y = fmaf(u1.z, bf16_lo(l2w[j].w), y), y = fmaf(u1.w, bf16_hi(l2w[j].w), y);
+            }
+        }
+        low[i * 128 + row] = y;
+        if (p.rank > 32 && i + 2 < mine) {
+#pragma unroll
+            for (int j = 0; j < 4; j++) l2w[j] = l2[j];
+        }
+    }
+    bar_arrive(5, 512);   // the epilogue warps wait for it
+}
+
 template <int kFmt, bool kOwn>
-__global__ void __launch_bounds__(kThreads, kOwn ? 2 : 1)
+__global__ void __launch_bounds__(product_threads(kOwn), 1)
     k_rows_product(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_s,
                    const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_l2,
                    const __grid_constant__ CUtensorMap tm_u, RowsParams p) {
@@ -493,6 +616,7 @@ __global__ void __launch_bounds__(kThreads, kOwn ? 2 : 1)
     const int S = p.stages;
     constexpr bool own = kOwn;
     const int split = (int)blockIdx.x, splits = (int)gridDim.x;       // parts of the channels
+    const int csize = splits * p.group, crank = (int)cluster_ctarank();   // in the cluster: those of `group` tiles
     const int o0 = (int)blockIdx.y * 128;
     const int m0 = (int)blockIdx.z * p.n_rows;
     const int nm = imin(p.n_rows, p.rows - m0);
@@ -500,42 +624,50 @@ __global__ void __launch_bounds__(kThreads, kOwn ? 2 : 1)
     const uint32_t b_all = (uint32_t)p.n_pad * 128u, b_bytes = own ? 0u : b_all;   // digits of a stage; those in the ring
     const uint32_t stage = kCodeBytes + b_bytes + kScaleBytes;        // codes, digits, the codes' scales
     uint8_t* digits = sm + (size_t)S * stage;                         // own digits: [stage][column][128 bytes]
-    const int total = nA + (split == 0 ? p.slab / 64 : 0);            // stages: the weight's, then the low-rank factor's
+    const int total = nA + (!own && split == 0 ? p.slab / 64 : 0);    // stages: the weight's, then the low-rank factor's
+    float* up = (float*)(digits + (own ? (size_t)p.own_stages * b_all : 0));   // own: [u_parts][8][rank] parts of U,
+    float* su = up + p.u_parts * 8 * p.rank;                          //   U, U L2
+    float* slow = su + 8 * p.rank;
     const uint32_t n16 = (uint32_t)(p.n_rows + 15) & ~15u;
     volatile int* abort_flag = &bars.abort_flag;
 
-    // the rows whose digits this CTA writes, before the weight's loads
-    Raw8<kFmt> raw[kOwnTurns];
-    if (own && warp >= 4) load_own_rows<kFmt>(p, a0 * 256, nA * 256, raw);
     if (tid == 0) {
         for (int s = 0; s < S; s++) {
             mbar_init(&bars.full[s], own ? 1 : 2);   // one producer, or both
             mbar_init(&bars.empty[s], 1);
         }
         for (int i = 0; i < kOwnTurns; i++) mbar_init(&bars.digits[i], kEpiThreads / 32);
+        mbar_init(&bars.u, (uint32_t)csize);
         mbar_init(&bars.accf, 1);
         bars.abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
-        tmem_alloc(&bars.tmem, (uint32_t)p.tmem_cols);
+        tmem_alloc(&bars.tmem, kTmemCols);
         tmem_relinquish();
     }
     if (warp == 0 && lane == 0) {
         prefetch_tmap(&tm_w);
         prefetch_tmap(&tm_s);
-        prefetch_tmap(&tm_l2);
-        prefetch_tmap(&tm_u);
-        if (!own) prefetch_tmap(&tm_x);
+        if (!own) {
+            prefetch_tmap(&tm_x);
+            prefetch_tmap(&tm_l2);
+            prefetch_tmap(&tm_u);
+        }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars.tmem, t_low = tmem + (uint32_t)p.d_cols, t_one = t_low + n16, t_sf = t_one + 8;
+    if (own) {
+        cluster_arrive();   // waited for before this CTA first touches another's shared memory
+        griddep_wait();     // with k_rows_prepare in front everything before that launch is done already
+    }
     griddep_launch();
 
     if (warp == 0) {
         // ------------------------------------------------ codes and their scales
+        if (own) bar_sync(3, 32 + 512);   // the loads of everything else are under way
         if (lane == 0) {
             const int half = (o0 >> 7) & 1, blk0 = (o0 >> 8) * (p.Ci / 64) + a0 * 4;
             Ring r;
@@ -550,11 +682,8 @@ __global__ void __launch_bounds__(kThreads, kOwn ? 2 : 1)
                     // 32 lanes x 16 bytes per 64-channel block: one half of the 256-row tile
                     tma_load_4d(dst + kCodeBytes + b_bytes, &tm_s, full, 0, half, 0, blk0 + 4 * g);
                 } else {
-                    // U lies in the place of the digits and the scales, 2 KB at least for 16 rows
-                    if (own && g == nA) griddep_wait();
-                    mbar_arrive_expect_tx(full, kCodeBytes + (own ? n16 * 128 : 0));
+                    mbar_arrive_expect_tx(full, kCodeBytes);
                     tma_load_2d(dst, &tm_l2, full, (g - nA) * 64, o0);
-                    if (own) tma_load_2d(dst + kCodeBytes, &tm_u, full, (g - nA) * 64, m0);
                 }
             }
             for (int q = g > S ? g - S : 0; q < g; q++)   // every copy lands before shared memory is released
@@ -571,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, kOwn ? 2 : 1)
                 uint64_t* full = &bars.full[r.slot];
                 if (g >= S && !mbar_wait(&bars.empty[r.slot], r.phase ^ 1, abort_flag, p.status, p.budget_ns)) break;
                 uint8_t* dst = sm + (size_t)r.slot * stage + kCodeBytes;
-                mbar_arrive_expect_tx(full, g < nA ? b_bytes : n16 * 128);
+                mbar_arrive_expect_tx(full, g < nA ? b_bytes : n16 * 128);   // U within the digits' and scales' places
                 if (g < nA)
                     tma_load_2d(dst, &tm_x, full, (a0 + g) * 128, m0 * kDigits);
                 else
@@ -637,12 +766,18 @@ __global__ void __launch_bounds__(kThreads, kOwn ? 2 : 1)
     const PackedHeader* hdr = reinterpret_cast<const PackedHeader*>(p.packed_w);
     bool done = true, ok = true;
     float S_W = 0.f;
+    const bool epi = warp >= 4 && warp < 12;
     uint32_t flags = 0;
     float bias = 0.f;
-    if (warp >= 4) {
+    if (own && warp < 4) cluster_wait();
+    if (own && warp >= 12) lowrank_term<kFmt>(p, bars, up, su, slow, o0, crank, csize, split, splits);
+    if (epi) {
+        Raw8<kFmt> raw[kOwnTurns];
+        if (own) load_own_rows<kFmt>(p, a0 * 256, nA * 256, raw);
         flags = hdr->flags;
         bias = *(const float*)(p.packed_w + p.off_bias + 4ll * (o0 + row));
         S_W = hdr->S_W;
+        if (own) bar_arrive(3, 32 + 512);   // the weight may follow
         if (warp < 8) {
             // the digits' scales: E4M3 1 in eight columns of every lane
             const uint32_t one = 0x38383838u;
@@ -651,26 +786,29 @@ __global__ void __launch_bounds__(kThreads, kOwn ? 2 : 1)
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            asm volatile("bar.arrive 2, 160;" ::: "memory");
+            bar_arrive(2, 32 + 128);
         }
         if (own) {
             write_own_digits<kFmt>(p, bars, digits, nA * 256, raw);
+            cluster_wait();
         } else {
             griddep_wait();   // the rows' factors come from k_rows_prepare
             if (et < nm) bars.e[et] = p.e[m0 + et];
         }
         bar_sync(1, kEpiThreads);
         ok = header_ok(p);
+        if (own) bar_sync(5, 512);   // the low-rank term
         if (lane == 0) done = mbar_wait(&bars.accf, 0, abort_flag, p.status, p.budget_ns);
         done = __shfl_sync(0xffffffffu, done, 0);
         tc_fence_after();
     }
+    if (own && tid == 96 && blockIdx.x + blockIdx.y + blockIdx.z == 0) *p.status = header_ok(p) ? 0 : kStatusBadWeight;
     const float bv = (flags & kPackedHasBias) ? bias : 0.f;
     // This CTA's part of the rows 4 b to 4 b + 3 for the thread's output channel: the digits' columns with
     // weights 8^-p, times S_W and the row's factor, and U L2 where this CTA has it
     auto parts_of = [&](int b, float (&v)[4]) {
         uint32_t acc[32], low[4];
-        if (split == 0) tmem_ld_x4(t_low + trow + (uint32_t)(4 * b), low);
+        if (!own && split == 0) tmem_ld_x4(t_low + trow + (uint32_t)(4 * b), low);
 #pragma unroll
         for (int c = 0; c < 32; c += 16) tmem_ld_x16(tmem + trow + (uint32_t)(32 * b + c), *reinterpret_cast<uint32_t(*)[16]>(&acc[c]));
         tmem_ld_wait();
@@ -679,34 +817,41 @@ __global__ void __launch_bounds__(kThreads, kOwn ? 2 : 1)
             v[i] = __uint_as_float(acc[kDigits * i + kDigits - 1]);
 #pragma unroll
             for (int q = kDigits - 2; q >= 0; q--) v[i] = fmaf(v[i], 0.125f, __uint_as_float(acc[kDigits * i + q]));
-            v[i] = fmaf(v[i] * S_W, bars.e[imin(4 * b + i, nm - 1)], split == 0 ? __uint_as_float(low[i]) : 0.f);
+            v[i] = fmaf(v[i] * S_W, bars.e[imin(4 * b + i, nm - 1)], !own && split == 0 ? __uint_as_float(low[i]) : 0.f);
         }
     };
-    // Y of the thread's output channel for the row m of the pass and the row m + step where `two` is set
-    auto finish = [&](int m, int step, bool two, float y0, float y1) {
+    // Y of the thread's output channel for the i-th of the rows split, split + splits, ... that this CTA finishes, and
+    // for the next where there is one
+    const int mine = split < nm ? (nm - split + splits - 1) / splits : 0;
+    auto finish = [&](int i, float y0, float y1) {
+        const int m = split + i * splits;
+        const bool two = i + 1 < mine;
         y0 += bv, y1 += bv;
+        if (own) y0 += slow[i * 128 + row], y1 += two ? slow[(i + 1) * 128 + row] : 0.f;
         if (p.gelu) f2_unpack(gelu_erf2(f2_pack(y0, y1)), y0, y1);
         uint16_t* dst = p.y + (long long)(m0 + m) * p.y_stride + o0 + row;
         dst[0] = f32_to_bf16_rn(y0);
-        if (two) dst[(long long)step * p.y_stride] = f32_to_bf16_rn(y1);
+        if (two) dst[(long long)splits * p.y_stride] = f32_to_bf16_rn(y1);
     };
     if (splits == 1) {
-        if (warp >= 4 && done && ok) {
+        if (epi && done && ok) {
             for (int b = group; 4 * b < nm; b += 2) {
                 float v[4];
                 parts_of(b, v);
-                finish(4 * b, 1, 4 * b + 1 < nm, v[0], v[1]);
-                if (4 * b + 2 < nm) finish(4 * b + 2, 1, 4 * b + 3 < nm, v[2], v[3]);
+                finish(4 * b, v[0], v[1]);
+                if (4 * b + 2 < nm) finish(4 * b + 2, v[2], v[3]);
             }
         }
+        __syncwarp();
+        if (own) cluster_sync();   // no CTA leaves while another still reads its part of U
     } else {
         // The parts of a tile: the CTA of part r sums, in the order of the parts, the rows m with m % splits = r.
         // The buffer takes the operand ring's place, so every CTA of the cluster is past its MMAs first.
         __syncwarp();
         cluster_sync();
         float* red = (float*)sm;   // [part][row / splits][128 output channels]
-        const int per = (nm + splits - 1) / splits;
-        if (warp >= 4 && done) {
+        const int per = (nm + splits - 1) / splits, tile0 = crank - split;
+        if (epi && done) {
             for (int b = group; 4 * b < nm; b += 2) {
                 float v[4];
                 parts_of(b, v);
@@ -714,22 +859,21 @@ __global__ void __launch_bounds__(kThreads, kOwn ? 2 : 1)
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     if (4 * b + i < nm)
-                        st_dsmem_f32(mapa_shared(smem_u32(&red[(split * per + at) * 128 + row]), (uint32_t)dst), v[i]);
+                        st_dsmem_f32(mapa_shared(smem_u32(&red[(split * per + at) * 128 + row]), (uint32_t)(tile0 + dst)), v[i]);
                     if (++dst == splits) dst = 0, at++;
                 }
             }
         }
         __syncwarp();
         cluster_sync();
-        if (warp >= 4 && done && ok) {
-            const int mine = split < nm ? (nm - split + splits - 1) / splits : 0;   // rows split, split + splits, ...
+        if (epi && done && ok) {
             for (int n = 2 * group; n < mine; n += 4) {
                 float v0 = 0.f, v1 = 0.f;
                 for (int q = 0; q < splits; q++) {
                     v0 += red[(q * per + n) * 128 + row];
                     if (n + 1 < mine) v1 += red[(q * per + n + 1) * 128 + row];
                 }
-                finish(split + n * splits, splits, n + 1 < mine, v0, v1);
+                finish(n, v0, v1);
             }
         }
     }
@@ -737,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, kOwn ? 2 : 1)
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
+        tmem_dealloc(tmem, kTmemCols);
     }
 }
 
@@ -781,12 +925,12 @@ auto by_format(int x_format, bool own, F f) {
 template <typename K>
 cudaError_t allow_smem(K kernel) {
     return once_per_device((const void*)kernel, [=] {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     });
 }
 
-// Clusters of `size` CTAs of the product, one CTA per SM, that fit on the current device at once (the same for all
-// forms), asked once per device and size.
+// Clusters of `size` CTAs of the product (one CTA per SM) that fit on the current device at once, the same for all
+// forms; asked once per device and size.
 cudaError_t resident_clusters(int size, int* clusters) {
     constexpr int kDevices = 64;
     static std::atomic<int> known[kDevices][9];
@@ -804,8 +948,8 @@ cudaError_t resident_clusters(int size, int* clusters) {
     attr[0].val.clusterDim.x = (unsigned)size;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3((unsigned)size, 1024);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kMaxSmem;
+    cfg.blockDim = dim3(product_threads(false));
+    cfg.dynamicSmemBytes = kSmem;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if ((e = cudaOccupancyMaxActiveClusters(clusters, kernel, &cfg)) != cudaSuccess) return e;
@@ -823,31 +967,35 @@ cudaError_t rows_plan(RowsParams& p) {
     p.n_pad = p.n_rows * kDigits;
     p.d_cols = (int)cdiv(p.n_pad, 32) * 32;
     const int tiles = p.Co / 128, k256 = p.Ci / 256, digits = p.n_pad * 128;
-    // Up to kOwnRows rows two CTAs share an SM (256 tensor-memory columns each) and write their digits
-    // themselves, if those and a ring of enough stages fit on half an SM, or else on a whole one.
-    for (int attempt = p.rows <= kOwnRows ? 0 : 2; attempt < 3; attempt++) {
-        const bool own = attempt < 2, small = attempt == 0;
-        // a cluster splits the channels as far as every CTA is still resident at once
-        p.splits = 1;
-        const int tries[] = {8, 6, 4, 3, 2};
+    for (int attempt = p.rows <= kOwnRows ? 0 : 1; attempt < 2; attempt++) {
+        // up to kOwnRows rows the product does everything, if the digits and a ring of enough stages fit
+        const bool own = attempt == 0;
+        // a cluster splits the channels as far as every CTA is still resident at once; with the low-rank term
+        // formed in it, it also takes as many tiles as fit, which then share the reading of L1
+        p.splits = 1, p.group = 0;
+        const int tries[] = {8, 6, 4, 3, 2, 1};
         for (int s : tries) {
-            int clusters = 0;
             if (s > k256) continue;
-            cudaError_t e = resident_clusters(s, &clusters);
-            if (e != cudaSuccess) return e;
-            if (tiles * p.passes <= clusters * (small ? 2 : 1)) {
-                p.splits = s;
-                break;
+            for (int g = own ? 8 / s : 1; g > 0 && !p.group; g--) {
+                int clusters = 0;
+                if (tiles % g) continue;
+                cudaError_t e = resident_clusters(s * g, &clusters);
+                if (e != cudaSuccess) return e;
+                if (tiles / g * p.passes <= clusters) p.splits = s, p.group = g;
             }
+            if (p.group) break;
         }
-        const int nA = (int)cdiv(k256, p.splits);
+        if (!p.group)   // more tiles than that: clusters of up to four of them for L1's sake
+            for (p.group = own ? 4 : 1; tiles % p.group; p.group--) {
+            }
+        const int items = p.rank / 16;
+        p.u_parts = items < 8 ? 8 / items : 1;
         p.own_digits = own;
-        p.tmem_cols = small ? 256 : 512;
-        p.smem = small ? kSmallSmem : kMaxSmem;
-        const int room = p.smem - 1024 - (own ? nA * digits : 0);
+        p.own_stages = (int)cdiv(k256, p.splits);
+        const int room = kSmem - 1024 - (own ? p.own_stages * digits + ((p.u_parts + 1) * 8 * p.rank + kOwnRows * 128) * 4 : 0);
         const int stage = (int)(kCodeBytes + kScaleBytes) + (own ? 0 : digits);
-        p.stages = room < 0 ? 0 : imin(imin(kStages, room / stage), (p.tmem_cols - p.d_cols - (int)cdiv(p.n_rows, 16) * 16 - 8) / 16);
-        if (own && (p.stages < imin(small ? 4 : 6, nA) || nA > kOwnTurns * own_warps(p.rows))) continue;
+        p.stages = room < 0 ? 0 : imin(imin(kStages, room / stage), ((int)kTmemCols - p.d_cols - (int)cdiv(p.n_rows, 16) * 16 - 8) / 16);
+        if (own && (p.stages < imin(6, p.own_stages) || p.own_stages > kOwnTurns * own_warps(p.rows))) continue;
         break;
     }
     return cudaSuccess;
@@ -861,25 +1009,31 @@ cudaError_t launch_rows(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const 
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = kPrepCluster;
-        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        attr[1].val.clusterDim.z = 1;
         cfg.stream = st;
         cfg.attrs = attr;
         cfg.numAttrs = 2;
-        const long long blocks = p.own_digits ? 0 : cdiv((long long)p.rows * cdiv(p.Ci, kBlockChannels), kPrepCluster);
-        cfg.gridDim = dim3((unsigned)((blocks + cdiv(p.rows, 16) * cdiv(p.rank, 32)) * kPrepCluster));
-        cfg.blockDim = dim3(kPrepThreads);
-        // the product's split of the SM between L1 and shared memory: a different one would keep its CTAs off an
-        // SM until this kernel's have left
-        cudaError_t e = once_per_device((const void*)prepare, [&] {
-            return cudaFuncSetAttribute(prepare, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-        });
-        if (e != cudaSuccess || (e = cudaLaunchKernelEx(&cfg, prepare, p)) != cudaSuccess) return e;
+        cudaError_t e;
+        if (!p.own_digits) {
+            // the product's split of the SM between L1 and shared memory: a different one would keep its CTAs off
+            // an SM until this kernel's have left
+            e = once_per_device((const void*)prepare, [&] {
+                return cudaFuncSetAttribute(prepare, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+            });
+            if (e != cudaSuccess) return e;
+            const long long blocks = cdiv((long long)p.rows * cdiv(p.Ci, kBlockChannels), kPrepCluster);
+            attr[1].val.clusterDim.x = kPrepCluster;
+            attr[1].val.clusterDim.y = 1;
+            cfg.gridDim = dim3((unsigned)((blocks + cdiv(p.rows, 16) * cdiv(p.rank, 32)) * kPrepCluster));
+            cfg.blockDim = dim3(kPrepThreads);
+            if ((e = cudaLaunchKernelEx(&cfg, prepare, p)) != cudaSuccess) return e;
+        }
         if ((e = allow_smem(product)) != cudaSuccess) return e;
         attr[1].val.clusterDim.x = (unsigned)p.splits;
+        attr[1].val.clusterDim.y = (unsigned)p.group;
         cfg.gridDim = dim3((unsigned)p.splits, (unsigned)(p.Co / 128), (unsigned)p.passes);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = (size_t)p.smem;
+        cfg.blockDim = dim3((unsigned)product_threads(p.own_digits != 0));
+        cfg.dynamicSmemBytes = kSmem;
         return cudaLaunchKernelEx(&cfg, product, tm_w, tm_s, tm_x, tm_l2, tm_u, p);
     });
 }
