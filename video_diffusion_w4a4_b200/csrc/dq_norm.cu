@@ -102,7 +102,7 @@ __device__ __forceinline__ void store_codes8(uint8_t* dst, int c0, int C, const 
 enum { kOutBf16 = 0, kOutRow = 1, kOutGroup = 2 };
 
 template <int kItems, bool kWarp, bool kWide, int kOut>
-__global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : 1024) k_rmsnorm(NormParams p) {
+__global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kItems == 2 ? 512 : 1024, kItems == 2 && !kWarp ? 3 : 1) k_rmsnorm(NormParams p) {
     __shared__ float sh[2][32];
     __shared__ double shd[32];
     const int T = kWarp ? 32 : (int)blockDim.x, t = kWarp ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
@@ -110,6 +110,8 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : 1024) k_rmsnorm(NormP
     if (kWarp && row >= p.rows) return;
     const uint16_t* x = p.x + row * p.x_stride;
     const uint16_t* r = p.residual + row * p.r_stride;
+    griddep_wait();     // X may come from the launch before this one
+    griddep_launch();
     uint32_t xw[kItems][4], rw[kItems][4];
 #pragma unroll
     for (int i = 0; i < kItems; i++) {
@@ -203,17 +205,23 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : 1024) k_rmsnorm(NormP
 }
 
 template <int kItems, bool kWarp, bool kWide>
-void launch(const NormParams& p, unsigned grid, unsigned threads, cudaStream_t st) {
-    if (!p.scales)
-        k_rmsnorm<kItems, kWarp, kWide, kOutBf16><<<grid, threads, 0, st>>>(p);
-    else if (!p.group)
-        k_rmsnorm<kItems, kWarp, kWide, kOutRow><<<grid, threads, 0, st>>>(p);
-    else
-        k_rmsnorm<kItems, kWarp, kWide, kOutGroup><<<grid, threads, 0, st>>>(p);
+cudaError_t launch(const NormParams& p, unsigned grid, unsigned threads, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (!p.scales) return cudaLaunchKernelEx(&cfg, k_rmsnorm<kItems, kWarp, kWide, kOutBf16>, p);
+    if (!p.group) return cudaLaunchKernelEx(&cfg, k_rmsnorm<kItems, kWarp, kWide, kOutRow>, p);
+    return cudaLaunchKernelEx(&cfg, k_rmsnorm<kItems, kWarp, kWide, kOutGroup>, p);
 }
 
 template <bool kWide>
-void launch_width(const NormParams& p, cudaStream_t st) {
+cudaError_t launch_width(const NormParams& p, cudaStream_t st) {
     const int pieces = (int)cdiv(p.C, 8);
     const unsigned warp_grid = (unsigned)cdiv(p.rows, kWarpRows);
     if (pieces <= 32) return launch<1, true, kWide>(p, warp_grid, 32 * kWarpRows, st);
@@ -223,7 +231,7 @@ void launch_width(const NormParams& p, cudaStream_t st) {
     const unsigned threads = (unsigned)(cdiv(cdiv(pieces, items), 32) * 32);
     if (items == 1) return launch<1, false, kWide>(p, (unsigned)p.rows, threads, st);
     if (items == 2) return launch<2, false, kWide>(p, (unsigned)p.rows, threads, st);
-    launch<kMaxItems, false, kWide>(p, (unsigned)p.rows, threads, st);
+    return launch<kMaxItems, false, kWide>(p, (unsigned)p.rows, threads, st);
 }
 
 }  // namespace
@@ -236,11 +244,7 @@ cudaError_t launch_rmsnorm(const NormParams& p, cudaStream_t st) {
     const bool w = p.C % 8 == 0 && wide(p.x, p.x_stride, 16) && wide(p.residual, p.residual ? p.r_stride : 0, 16) &&
                    wide(p.gamma, 0, 16) && wide(p.sum, p.sum ? p.s_stride : 0, 16) &&
                    wide(p.y, p.y_stride, p.scales ? 8 : 16);
-    if (w)
-        launch_width<true>(p, st);
-    else
-        launch_width<false>(p, st);
-    return cudaGetLastError();
+    return w ? launch_width<true>(p, st) : launch_width<false>(p, st);
 }
 
 }  // namespace dq

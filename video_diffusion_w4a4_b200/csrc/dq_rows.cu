@@ -63,9 +63,6 @@ constexpr uint32_t kTmemCols = 512;
 
 // ------------------------------------------------------------------ small pieces
 
-__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void bar_arrive(int id, int nthreads) {
@@ -300,26 +297,33 @@ __device__ __forceinline__ void load_rows_16(const RowsParams& p, int m0, int nm
     }
 }
 
-constexpr int kPrepThreads = 1024, kPrepCluster = 8, kBlockChannels = 8 * kPrepThreads;
+// k_rows_prepare's CTAs: eight channels a thread, a row in as few of them as that allows.  Then a warp of a low-rank
+// cluster has one 64-channel block, too.
+constexpr int kPrepThreads = 1024, kPrepCluster = 8;
+__host__ __device__ inline int prep_parts(int Ci) { return (Ci + 8 * kPrepThreads - 1) / (8 * kPrepThreads); }
+inline int prep_threads(int Ci) {
+    const int warps = (int)cdiv(Ci, 256 * prep_parts(Ci));
+    return 32 * (warps < 8 ? 8 : warps);
+}
 
-// Digits of 8192 channels of a row.  Each block finds the row's largest magnitude for itself: a second read of at
-// most 28 KB, from L2, costs less than a hand-off between blocks.
+// Digits of the channels of a row that one CTA has.  Each block finds the row's largest magnitude for itself: a
+// second read of at most 28 KB, from L2, costs less than a hand-off between blocks.
 template <int kFmt>
 __device__ __forceinline__ void digits_block(const RowsParams& p, int m, int part) {
     __shared__ float sh[kPrepThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, c = part * kBlockChannels + tid * 8;
-    float am = 0.f;
+    const int tid = threadIdx.x, lane = tid & 31, channels = 8 * (int)blockDim.x, c = part * channels + tid * 8;
     Raw8<kFmt> raw = {};
     if (c < p.Ci) raw = load_raw8<kFmt>(p, m, c);
-    for (int i = tid * 8; i < p.Ci; i += kBlockChannels) am = max_nan(am, amax8<kFmt>(load_raw8<kFmt>(p, m, i)));
+    float am = amax8<kFmt>(raw);
+    for (int i = tid * 8; i < p.Ci; i += channels)
+        if (i != c) am = max_nan(am, amax8<kFmt>(load_raw8<kFmt>(p, m, i)));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
     if (lane == 0) sh[tid >> 5] = am;
     __syncthreads();
     griddep_launch();   // the block's loads have arrived
     am = sh[0];
-#pragma unroll
-    for (int w = 1; w < kPrepThreads / 32; w++) am = max_nan(am, sh[w]);
+    for (int w = 1; w < (int)blockDim.x / 32; w++) am = max_nan(am, sh[w]);
     const bool finite = finite_row(am);
     const int k = unit_exponent(am);
     if (part == 0 && tid == 0) p.e[m] = row_factor<kFmt>(p, m, k, finite);
@@ -385,7 +389,7 @@ __device__ __forceinline__ void lowrank_store(float* dst, int rank, int g, int t
 }
 
 // U of 16 rows and 32 ranks by a cluster of eight CTAs, an eighth of the channels each: a warp takes 16 of the ranks
-// and every sixteenth 64-channel block.  The sums are joined in rank order through distributed shared memory and
+// and one 64-channel block (every so manieth, past 8192 channels).  The sums are joined in rank order through distributed shared memory and
 // kept as BF16 hi + lo, 2^-17 of the value.
 template <int kFmt>
 __device__ __forceinline__ void lowrank_cluster(const RowsParams& p, int index, float (*wpart)[16][32], float (*part)[32]) {
@@ -393,23 +397,22 @@ __device__ __forceinline__ void lowrank_cluster(const RowsParams& p, int index, 
     const int crank = (int)cluster_ctarank(), rgroups = (p.rank + 31) / 32;
     const int m0 = index / rgroups * 16, nm = imin(16, p.rows - m0), j0 = index % rgroups * 32;
     const int nblk = p.Ci / 64, b0 = nblk * crank / kPrepCluster, b1 = nblk * (crank + 1) / kPrepCluster;
-    const int jw = j0 + 16 * (warp & 1), ks = warp >> 1;
+    const int jw = j0 + 16 * (warp & 1), ks = warp >> 1, nks = (int)blockDim.x >> 6, warps = (int)blockDim.x >> 5;
     float acc[2][4] = {};
-    if (jw < p.rank) {
-        for (int b = b0 + ks; b < b1; b += 16) {
+    if (jw < p.rank && ks < nks) {
+        for (int b = b0 + ks; b < b1; b += nks) {
             LowRankBlock<false> q;
             lowrank_load<kFmt, false>(p, m0, nm, jw, b, true, g, t, q);
             lowrank_add<kFmt, false>(q, acc);
         }
     }
-    lowrank_store<false>(&wpart[ks][0][16 * (warp & 1)], 32, g, t, acc);
+    if (ks < nks) lowrank_store<false>(&wpart[ks][0][16 * (warp & 1)], 32, g, t, acc);
     __syncthreads();
     griddep_launch();   // the CTA's loads have arrived
-    if (warp < 16) {
+    for (int m = warp; m < 16; m += warps) {
         float u = 0.f;
-#pragma unroll
-        for (int k = 0; k < 16; k++) u += wpart[k][warp][lane];
-        part[warp][lane] = u;
+        for (int k = 0; k < nks; k++) u += wpart[k][m][lane];
+        part[m][lane] = u;
     }
     cluster_sync();
     // an eighth of the sums per CTA: two rows
@@ -437,7 +440,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_rows_prepare(RowsParams p) {
     griddep_wait();     // the launch before this one may still read the workspace, or write X
     __shared__ float wpart[16][16][32], part[16][32];
     // the low-rank clusters first: they take longest
-    const int parts = (p.Ci + kBlockChannels - 1) / kBlockChannels, b = (int)blockIdx.x;
+    const int parts = prep_parts(p.Ci), b = (int)blockIdx.x;
     const int low = (p.rows + 15) / 16 * ((p.rank + 31) / 32) * kPrepCluster;
     if (b == 0 && threadIdx.x == 0) *p.status = header_ok(p) ? 0 : kStatusBadWeight;
     if (b < low)
@@ -711,49 +714,57 @@ __global__ void __launch_bounds__(product_threads(kOwn), 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ------------------------------------------------ MMAs (one elected lane; the warp's control flow is uniform)
-        const uint32_t idesc = idesc_nvfp4(128, p.n_pad), id_low = idesc_bf16(128, (int)n16);
-        const uint32_t base = smem_u32(sm);
+        // ------------------------------------------------ MMAs, by one lane throughout
         bar_sync(2, 32 + 128);   // the digits' scales are in tensor memory
         tc_fence_after();
-        Ring r;
-        uint32_t sa = base, ta = t_sf, sb = own ? smem_u32(digits) : base + kCodeBytes;
-        const uint32_t b_step = own ? b_all : stage;
-        int turn = 0, left = 0;                          // own digits: stages until the next turn's barrier
-        for (int g = 0; g < total; g++) {
-            if (own && g < nA && left-- == 0) {
-                if (!__all_sync(0xffffffffu, mbar_wait_spin(&bars.digits[turn], 0, abort_flag, p.status, p.budget_ns))) break;
-                turn++;
-                left = own_warps(p.rows) - 1;
-            }
-            if (!__all_sync(0xffffffffu, mbar_wait_spin(&bars.full[r.slot], r.phase, abort_flag, p.status, p.budget_ns))) break;
-            tc_fence_after();
-            if (elect_one()) {
-                const uint64_t ad = desc_k_sw128(sa);
-                if (g < nA) {
-                    const uint64_t bd = desc_k_sw128(sb), fa = smem_desc(sa + kCodeBytes + b_bytes, 128, 128, 0);
-                    // the stage's own columns: nothing still reads them, as its empty barrier was waited for
-#pragma unroll
-                    for (int j = 0; j < 4; j++) tmem_cp_32x128b(ta + 4 * j, fa + 32 * j);
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        mma_nvfp4(tmem, ad + 2 * j, bd + 2 * j, idesc, ta + 4 * j, t_one, (g | j) != 0);
-                } else {
-                    const uint64_t bd = desc_k_sw128(sa + kCodeBytes);
-#pragma unroll
-                    for (int j = 0; j < 4; j++) mma_bf16(t_low, ad + 2 * j, bd + 2 * j, id_low, (g > nA || j) ? 1u : 0u);
-                }
-                tc_commit(&bars.empty[r.slot]);
-            }
-            __syncwarp();
-            sa += stage, ta += 16, sb += b_step;
-            r.next(S);
-            if (r.slot == 0) {
-                sa = base, ta = t_sf;
-                if (!own) sb = base + kCodeBytes;
-            }
-        }
         if (elect_one()) {
+            const uint32_t idesc = idesc_nvfp4(128, p.n_pad), id_low = idesc_bf16(128, (int)n16);
+            // descriptors: the address field is the offset / 16, so a step is an addition
+            const uint32_t base = smem_u32(sm), step = stage >> 4, b_step = own ? b_all >> 4 : step;
+            const uint64_t a0d = desc_k_sw128(base), b0d = desc_k_sw128(own ? smem_u32(digits) : base + kCodeBytes),
+                           f0d = smem_desc(base + kCodeBytes + b_bytes, 128, 128, 0);
+            Ring r;
+            uint64_t ad = a0d, bd = b0d, fd = f0d;
+            uint32_t ta = t_sf, more = 0;
+            int turn = 0, left = 0, g = 0;                   // own digits: stages until the next turn's barrier
+            const int per = own_warps(p.rows);
+            for (; g < nA; g++) {
+                if (own && left-- == 0) {
+                    if (!mbar_wait_spin(&bars.digits[turn], 0, abort_flag, p.status, p.budget_ns)) break;
+                    turn++;
+                    left = per - 1;
+                }
+                if (!mbar_wait_spin(&bars.full[r.slot], r.phase, abort_flag, p.status, p.budget_ns)) break;
+                tc_fence_after();
+                // the stage's own columns: nothing still reads them, as its empty barrier was waited for
+#pragma unroll
+                for (int j = 0; j < 4; j++) tmem_cp_32x128b(ta + 4 * j, fd + 32 * j);
+                mma_nvfp4(tmem, ad, bd, idesc, ta, t_one, more);
+                more = 1;
+#pragma unroll
+                for (int j = 1; j < 4; j++) mma_nvfp4(tmem, ad + 2 * j, bd + 2 * j, idesc, ta + 4 * j, t_one, 1u);
+                tc_commit(&bars.empty[r.slot]);
+                ad += step, bd += b_step, fd += step, ta += 16;
+                r.next(S);
+                if (r.slot == 0) {
+                    ad = a0d, fd = f0d, ta = t_sf;
+                    if (!own) bd = b0d;
+                }
+            }
+            if (!own && g == nA) {
+                more = 0;
+                for (; g < total; g++) {
+                    if (!mbar_wait_spin(&bars.full[r.slot], r.phase, abort_flag, p.status, p.budget_ns)) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int j = 0; j < 4; j++) mma_bf16(t_low, ad + 2 * j, bd + 2 * j, id_low, more | (uint32_t)j);
+                    more = 1;
+                    tc_commit(&bars.empty[r.slot]);
+                    ad += step, bd += step;
+                    r.next(S);
+                    if (r.slot == 0) ad = a0d, bd = b0d;
+                }
+            }
             tc_commit(&bars.accf);
             mbar_wait(&bars.accf, 0, abort_flag, nullptr, p.budget_ns, false);   // no MMA runs past this point
         }
@@ -1021,11 +1032,11 @@ cudaError_t launch_rows(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const 
                 return cudaFuncSetAttribute(prepare, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
             });
             if (e != cudaSuccess) return e;
-            const long long blocks = cdiv((long long)p.rows * cdiv(p.Ci, kBlockChannels), kPrepCluster);
+            const long long blocks = cdiv((long long)p.rows * prep_parts(p.Ci), kPrepCluster);
             attr[1].val.clusterDim.x = kPrepCluster;
             attr[1].val.clusterDim.y = 1;
             cfg.gridDim = dim3((unsigned)((blocks + cdiv(p.rows, 16) * cdiv(p.rank, 32)) * kPrepCluster));
-            cfg.blockDim = dim3(kPrepThreads);
+            cfg.blockDim = dim3((unsigned)prep_threads(p.Ci));
             if ((e = cudaLaunchKernelEx(&cfg, prepare, p)) != cudaSuccess) return e;
         }
         if ((e = allow_smem(product)) != cudaSuccess) return e;
