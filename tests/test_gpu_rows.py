@@ -378,6 +378,149 @@ def test_rows_on_two_streams(dq):
     assert all(torch.equal(y.cpu(), r) for y, r in zip(ys, want))
 
 
+# ------------------------------------------------------------------ cuts of the product, order of launches
+
+@pytest.mark.parametrize("rows", range(1, 10))
+@pytest.mark.parametrize("Ci,Co,rank", [(256, 1280, 112), (1536, 2560, 32), (7168, 256, 16), (5120, 768, 80)])
+def test_few_rows_of_every_count(dq, Ci, Co, rank, rows):
+    """One row to one more than a single launch takes, in layers that are cut into clusters in different ways."""
+    w, dev = weight(dq, Ci, Co, rank, seed=Ci, bias=True)
+    for fmt in (0, 1, 2):
+        v, x, sc = rows_input(rows, Ci, fmt, seed=10 * rows + fmt)
+        ref, tol = rows_reference(w, v, fmt == 2)
+        assert_within(run_rows(dq, dev, w, x, sc, fmt, gelu=fmt == 2, y_pad=rows % 2), ref, tol, "Y")
+
+
+@pytest.mark.parametrize("rows", [4, 40])
+def test_rows_with_scales_that_are_not_finite(dq, rows):
+    w, dev = weight(dq, 512, 768, 32, seed=512)
+    v, x, sc = rows_input(rows, 512, 1)
+    sc[0], sc[2] = float("inf"), float("-inf")
+    y = run_rows(dq, dev, w, x, sc, 1)
+    ref, tol = rows_reference(w, v, False)
+    fine = [m for m in range(rows) if m not in (0, 2)]
+    assert torch.isnan(y[0].float()).all() and torch.isnan(y[2].float()).all()
+    assert_within(y[fine], ref[fine], tol[fine], "Y")
+    v, x, sc = rows_input(rows, 512, 2)
+    sc[1, 3] = float("inf")
+    y = run_rows(dq, dev, w, x, sc, 2)
+    ref, tol = rows_reference(w, v, False)
+    fine = [m for m in range(rows) if m != 1]
+    assert torch.isnan(y[1].float()).all()
+    assert_within(y[fine], ref[fine], tol[fine], "Y")
+
+
+@pytest.mark.parametrize("rows", [1, 8, 30])
+def test_a_chain_without_waits_is_the_chain_with_waits(dq, rows):
+    """Blocks one after another on one stream, each on the output of the one before, all through the same buffers:
+    every launch has to wait for what it reads and for the readers of what it writes."""
+    C, F = 512, 1024
+    _, updev = weight(dq, C, F, 32, seed=21, bias=True)
+    _, downdev = weight(dq, F, C, 48, seed=22, bias=True)
+    x, r, g = norm_input(rows, C, True, True, seed=rows)
+    gd, st = g.cuda(), torch.cuda.Stream()
+    ws = torch.zeros(max(dq.dq_rows_workspace_bytes(rows, C, F, 32), dq.dq_rows_workspace_bytes(rows, F, C, 48)),
+                     dtype=torch.uint8, device="cuda")
+    q, sd = torch.zeros(rows, C, dtype=torch.float8_e4m3fn, device="cuda"), torch.zeros(rows, C // 64, device="cuda")
+    hid = torch.zeros(rows, F, dtype=torch.bfloat16, device="cuda")
+    ends = []
+    for wait in (True, False, False):
+        y, res = x.cuda(), r.cuda()
+        torch.cuda.synchronize()
+        for _ in range(12):
+            for step in range(3):
+                if step == 0:
+                    dq.dq_rmsnorm_forward(y, rows, C, q, residual=res, sum_out=res, gamma=gd,
+                                          y_format=dq.DQ_ROWS_E4M3_GROUP64, y_scales=sd, stream=st)
+                elif step == 1:
+                    dq.dq_rows_forward(q, rows, C, F, 32, *updev, hid, ws, ws.numel(), x_format=dq.DQ_ROWS_E4M3_GROUP64,
+                                       x_scales=sd, epilogue=dq.DQ_EPILOGUE_GELU, stream=st)
+                else:
+                    dq.dq_rows_forward(hid, rows, F, C, 48, *downdev, y, ws, ws.numel(), stream=st)
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert dq.dq_read_device_status(ws, st) == 0
+        ends.append((y.cpu(), res.cpu()))
+    assert torch.isfinite(ends[0][0].float()).all()
+    for y, res in ends[1:]:
+        assert torch.equal(y, ends[0][0]) and torch.equal(res, ends[0][1])
+
+
+def test_two_captured_calls_with_workspaces_of_their_own_overlap(dq):
+    w, dev = weight(dq, 2816, 512, 64, seed=2816, bias=True)
+    graphs, ys, want = [], [], []
+    for i, rows in enumerate((5, 33)):
+        _, x, _ = rows_input(rows, 2816, 0, seed=40 + i)
+        want.append(run_rows(dq, dev, w, x, None, 0))
+        xd, st, graph = x.cuda(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        ys.append(torch.zeros(rows, 512, dtype=torch.bfloat16, device="cuda"))
+        ws = torch.zeros(dq.dq_rows_workspace_bytes(rows, 2816, 512, 64), dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=st):
+            for _ in range(3):
+                dq.dq_rows_forward(xd, rows, 2816, 512, 64, *dev, ys[i], ws, ws.numel(), stream=st)
+        graphs.append((graph, st, xd, ws))
+    for _ in range(5):
+        for y in ys:
+            y.zero_()
+        torch.cuda.synchronize()
+        for graph, st, _, _ in graphs:
+            with torch.cuda.stream(st):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y.cpu(), r) for y, r in zip(ys, want))
+    graphs.clear()
+
+
+FIRST_CALL = """
+import sys
+import torch
+import video_diffusion_w4a4_b200 as dq
+from rows_case import Weight, rows_input
+rows, fmt = int(sys.argv[1]), 1
+w = Weight(dq, 512, 768, 32, seed=3, bias=True)
+dev = w.device()
+_, x, sc = rows_input(rows, 512, fmt, seed=4)
+xd, sd = x.cuda(), sc.cuda()
+h = torch.ones(rows, 768, dtype=torch.bfloat16, device="cuda")
+y, n = torch.zeros_like(h), torch.zeros_like(h)
+ws = torch.zeros(dq.dq_rows_workspace_bytes(rows, 512, 768, 32), dtype=torch.uint8, device="cuda")
+st, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+
+
+def calls():
+    dq.dq_rows_forward(xd, rows, 512, 768, 32, *dev, y, ws, ws.numel(), x_format=fmt, x_scales=sd, stream=st)
+    dq.dq_rmsnorm_forward(y, rows, 768, n, residual=h, stream=st)
+
+
+with torch.cuda.graph(graph, stream=st):
+    calls()
+graph.replay()
+torch.cuda.synchronize()
+first = y.clone(), n.clone()
+y.zero_(), n.zero_()
+calls()
+torch.cuda.synchronize()
+assert torch.equal(first[0], y) and torch.equal(first[1], n) and bool((y != 0).any())
+del graph
+print("captured first")
+"""
+
+
+@pytest.mark.parametrize("rows", [2, 20])
+def test_the_first_call_of_a_process_may_be_captured(rows):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([root, os.path.join(root, "tests"), os.environ.get("PYTHONPATH", "")]))
+    out = subprocess.run([sys.executable, "-c", FIRST_CALL, str(rows)], env=env, cwd=root, capture_output=True, text=True,
+                         timeout=240)
+    assert out.returncode == 0 and "captured first" in out.stdout, out.stdout + out.stderr
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("fmt", [0, 1, 2])

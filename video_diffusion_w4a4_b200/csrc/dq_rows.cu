@@ -242,16 +242,20 @@ __device__ __forceinline__ int unit_exponent(float am) {
     return (e ? e - 127 : -126) - 1;
 }
 
+__device__ __forceinline__ bool finite_row(float am) { return am < __int_as_float(0x7F800000); }
+
 // What a row's sum of digits is multiplied by: its unit 2^k, with the row's scale where the format has one; NaN
-// for a row with a NaN or an infinity, whose digits are zeros.
+// for a row with a NaN or an infinity (in its values, whose digits are then zeros, or its scale).
 template <int kFmt>
 __device__ __forceinline__ float row_factor(const RowsParams& p, int m, int k, bool finite) {
     float E = k >= -126 ? pow2i(k) : __int_as_float(1 << (k + 149));
-    if (kFmt == DQ_ROWS_E4M3) E *= p.x_scales[m];
+    if (kFmt == DQ_ROWS_E4M3) {
+        const float s = p.x_scales[m];
+        finite = finite && finite_row(fabsf(s));
+        E *= s;
+    }
     return finite ? E : __int_as_float(0x7FC00000);
 }
-
-__device__ __forceinline__ bool finite_row(float am) { return am < __int_as_float(0x7F800000); }
 
 // 2^-k in two exact steps (k in [-127, 126])
 struct Scale2 {
