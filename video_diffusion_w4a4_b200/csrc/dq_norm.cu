@@ -11,6 +11,14 @@
 // Eight neighbouring lanes hold 64 channels, so a group's maximum is three
 // shuffles.  Pointers, strides and widths that do not allow 16-byte pieces take
 // the same code with element accesses.
+//
+// Measured on B200, residual added and stored, calls one after another:
+// 32760 x 5120 to BF16 200 us (6.7 TB/s, the rate of a plain copy), 1560 x 5120 to
+// E4M3 with group scales 13.9 us (4.0 TB/s; its bytes alone 8.6 us, the rest the
+// launch, programmatic, 16.4 us without, and the last rows of 2.1 waves of CTAs).
+// Rows of 257 to 1024 pieces take two a thread in CTAs of at most 512 threads,
+// three or more to an SM: one piece a thread takes 16.9 us and 260 us, four CTAs'
+// worth of registers (32) 14.9 and 222 us, gamma loaded before the sum 14.1 and 224 us.
 #include <math.h>
 
 #include "dq_common.h"

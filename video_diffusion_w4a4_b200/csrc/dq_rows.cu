@@ -30,11 +30,31 @@
 // and whole ones, take a share of the channels of U each and exchange their sums
 // through distributed shared memory, so that L1 is read once a cluster.
 //
+// Bound: the weight's bytes (HBM) up to some 30 rows, then the digits' traffic from
+// L2 to the SMs, 4 bytes a value of X and tile of 128 output channels.  Measured on
+// B200, calls one after another on weights that are not in L2, against the time that
+// the bytes of weight, factors, X and Y need at the HBM's copy rate:
+//   1 x 5120 -> 5120     9.4 us (2.4)      1 x 5120 -> 13824   13.7 us (6.3)
+//   4 x 13824 -> 5120   15.9 us (6.3)     21 x 5120 -> 13824   16.0 us (6.4)
+//   77 x 2048 -> 5120   11.9 us (1.3)    512 x 5120 -> 5120    71 us (4.0; 16 at the
+//   BF16 tensor rate)
+// The stream alone, the same copies without any MMAs, takes 3.3 us for 5120 -> 5120
+// and 7.1 us for 5120 -> 13824 (5.6 TB/s); a launch that waits for the one before it
+// starts some 2.7 us after that one's last CTA has left (1.7 us until its wait
+// returns, 1 us of setup), the first stage arrives 1.5 us later, and the output is
+// written 1.3 to 1.9 us after the last MMA.  At 512 rows the product's 55 us move 669 MB
+// from L2 to the SMs (12 TB/s, with the tensor pipe busy 46 % of the time).
+//
+// MMAs: the four scale copies and four MMAs of a stage of 256 channels take 183
+// cycles with 8 columns, 336 with 168 and 512 with 256 (the tensor pipe's full rate),
+// issued by one lane without a pause.
+//
 // Once the weight streams, a load of anything else waits behind it for 2 to 4 us, a
 // ring of the weight's stages per SM deep.  So the other loads come first, or where
 // nothing waits for them: k_rows_product holds the stream back until they are under
-// way, and k_rows_prepare lets the product in when its own have arrived
-// (programmatic launch).
+// way (5120 -> 5120: 9.4 us against 9.8 us without; 5120 -> 13824: 13.7 against 13.1,
+// 13824 -> 5120 with 4 rows the same either way), and k_rows_prepare lets the product
+// in when its own have arrived (programmatic launch).
 #include "../../include/deltaquant.h"
 #include "dq_common.h"
 #include "dq_internal.h"
@@ -49,7 +69,11 @@ namespace {
 constexpr int kDigits = 8;                       // FP4 digits of a value
 constexpr int kPassRows = 32;                    // rows of X per CTA: 256 MMA columns
 constexpr int kOwnRows = 8;                      // up to so many rows the product writes the digits itself
-constexpr int kOwnTurns = 10;                    // pieces of eight channels a thread holds for that
+constexpr int kOwnTurns = 10;                    // pieces of eight channels a thread holds for that at most
+// ... and uses: with a warp to a row seven of them take longer than k_rows_prepare (8 rows, 5120 -> 5120: 12.2 us
+// against 11.2 us), one does not (1536 -> 1536: 8.1 us against 8.9 us); with two warps or more to a row ten do not
+// either (4 rows, 5120 -> 13824: 14.2 us against 14.7 us; 13824 -> 5120: 16.0 us against 18.4 us).
+constexpr int own_turns(int rows) { return rows <= 4 ? kOwnTurns : 4; }
 // producers of A and B, MMA, a spare warp, eight epilogue warps; eight for the low-rank term
 constexpr int product_threads(bool own) { return own ? 640 : 384; }
 constexpr int kEpiThreads = 256;
@@ -303,6 +327,8 @@ __device__ __forceinline__ void load_rows_16(const RowsParams& p, int m0, int nm
 
 // k_rows_prepare's CTAs: eight channels a thread, a row in as few of them as that allows.  Then a warp of a low-rank
 // cluster has one 64-channel block, too.
+// (77 rows of 2048: 11.9 us for the call, 14.8 us with 1024 threads whatever the row; 512 threads whatever the row
+// cost 512 rows of 5120 7 us.)
 constexpr int kPrepThreads = 1024, kPrepCluster = 8;
 __host__ __device__ inline int prep_parts(int Ci) { return (Ci + 8 * kPrepThreads - 1) / (8 * kPrepThreads); }
 inline int prep_threads(int Ci) {
@@ -1010,7 +1036,7 @@ cudaError_t rows_plan(RowsParams& p) {
         const int room = kSmem - 1024 - (own ? p.own_stages * digits + ((p.u_parts + 1) * 8 * p.rank + kOwnRows * 128) * 4 : 0);
         const int stage = (int)(kCodeBytes + kScaleBytes) + (own ? 0 : digits);
         p.stages = room < 0 ? 0 : imin(imin(kStages, room / stage), ((int)kTmemCols - p.d_cols - (int)cdiv(p.n_rows, 16) * 16 - 8) / 16);
-        if (own && (p.stages < imin(6, p.own_stages) || p.own_stages > kOwnTurns * own_warps(p.rows))) continue;
+        if (own && (p.stages < imin(6, p.own_stages) || p.own_stages > own_turns(p.rows) * own_warps(p.rows))) continue;
         break;
     }
     return cudaSuccess;
