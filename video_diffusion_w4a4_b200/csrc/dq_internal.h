@@ -143,6 +143,8 @@ struct RowsParams {
     int stages, d_cols;
     int own_digits, own_stages; // the product writes the digits itself (of up to so many 256-channel stages), and U L2
     int u_parts;                //   parts of a CTA's channels of U
+    int prep_cluster;           // else k_rows_prepare's CTAs
+    long long prep_ctas;
 };
 cudaError_t rows_plan(RowsParams& p);
 cudaError_t launch_rows(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const CUtensorMap& tm_x,

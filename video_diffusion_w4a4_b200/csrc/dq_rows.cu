@@ -36,7 +36,7 @@
 // the bytes of weight, factors, X and Y need at the HBM's copy rate:
 //   1 x 5120 -> 5120     9.4 us (2.4)      1 x 5120 -> 13824   13.7 us (6.3)
 //   4 x 13824 -> 5120   15.9 us (6.3)     21 x 5120 -> 13824   16.0 us (6.4)
-//   77 x 2048 -> 5120   11.9 us (1.3)    512 x 5120 -> 5120    71 us (4.0; 16 at the
+//   77 x 2048 -> 5120   12.0 us (1.3)    512 x 5120 -> 5120    62 us (4.0; 16 at the
 //   BF16 tensor rate)
 // The stream alone, the same copies without any MMAs, takes 3.3 us for 5120 -> 5120
 // and 7.1 us for 5120 -> 13824 (5.6 TB/s); a launch that waits for the one before it
@@ -327,7 +327,7 @@ __device__ __forceinline__ void load_rows_16(const RowsParams& p, int m0, int nm
 
 // k_rows_prepare's CTAs: eight channels a thread, a row in as few of them as that allows.  Then a warp of a low-rank
 // cluster has one 64-channel block, too.
-// (77 rows of 2048: 11.9 us for the call, 14.8 us with 1024 threads whatever the row; 512 threads whatever the row
+// (77 rows of 2048: 12 us for the call, 14.8 us with 1024 threads whatever the row; 512 threads whatever the row
 // cost 512 rows of 5120 7 us.)
 constexpr int kPrepThreads = 1024, kPrepCluster = 8;
 __host__ __device__ inline int prep_parts(int Ci) { return (Ci + 8 * kPrepThreads - 1) / (8 * kPrepThreads); }
@@ -336,35 +336,48 @@ inline int prep_threads(int Ci) {
     return 32 * (warps < 8 ? 8 : warps);
 }
 
-// Digits of the channels of a row that one CTA has.  Each block finds the row's largest magnitude for itself: a
-// second read of at most 28 KB, from L2, costs less than a hand-off between blocks.
+// Digits of the pieces (a row's channels that one CTA has at once) first, first + step, ... of all.  A CTA finds the
+// row's largest magnitude for itself: a second read of at most 28 KB, from L2, costs less than a hand-off between
+// CTAs.  The next piece's loads are under way beside this one's digits.
 template <int kFmt>
-__device__ __forceinline__ void digits_block(const RowsParams& p, int m, int part) {
-    __shared__ float sh[kPrepThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, channels = 8 * (int)blockDim.x, c = part * channels + tid * 8;
-    Raw8<kFmt> raw = {};
-    if (c < p.Ci) raw = load_raw8<kFmt>(p, m, c);
-    float am = amax8<kFmt>(raw);
-    for (int i = tid * 8; i < p.Ci; i += channels)
-        if (i != c) am = max_nan(am, amax8<kFmt>(load_raw8<kFmt>(p, m, i)));
+__device__ __forceinline__ void digits_blocks(const RowsParams& p, int first, int step) {
+    __shared__ float sh[2][kPrepThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, channels = 8 * (int)blockDim.x, parts = prep_parts(p.Ci), all = p.rows * parts;
+    if (first >= all) return;
+    int m = parts == 1 ? first : first / parts, c = (first - m * parts) * channels + tid * 8;
+    Raw8<kFmt> next = {};
+    if (c < p.Ci) next = load_raw8<kFmt>(p, m, c);
+    for (int at = first, turn = 0; at < all; turn ^= 1) {
+        const Raw8<kFmt> raw = next;
+        const int row = m, here = c;
+        float am = amax8<kFmt>(raw);
+        if (parts > 1)
+            for (int i = tid * 8; i < p.Ci; i += channels)
+                if (i != here) am = max_nan(am, amax8<kFmt>(load_raw8<kFmt>(p, row, i)));
+        if ((at += step) < all) {
+            m = parts == 1 ? at : at / parts, c = (at - m * parts) * channels + tid * 8;
+            next = {};
+            if (c < p.Ci) next = load_raw8<kFmt>(p, m, c);
+        }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
-    if (lane == 0) sh[tid >> 5] = am;
-    __syncthreads();
-    griddep_launch();   // the block's loads have arrived
-    am = sh[0];
-    for (int w = 1; w < (int)blockDim.x / 32; w++) am = max_nan(am, sh[w]);
-    const bool finite = finite_row(am);
-    const int k = unit_exponent(am);
-    if (part == 0 && tid == 0) p.e[m] = row_factor<kFmt>(p, m, k, finite);
-    if (c >= p.Ci) return;
-    float v[8];
-    uint64_t v2[4];
-    values8<kFmt>(raw, v);
-    scaled_pairs(v, inv_scale(k), finite, v2);
-    uint8_t* dst = p.digits + (size_t)m * kDigits * (p.Ci / 2) + c / 2;
+        for (int o = 16; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
+        if (lane == 0) sh[turn][tid >> 5] = am;
+        __syncthreads();
+        if (at >= all) griddep_launch();   // the CTA's loads have arrived
+        am = sh[turn][0];
+        for (int w = 1; w < (int)blockDim.x / 32; w++) am = max_nan(am, sh[turn][w]);
+        const bool finite = finite_row(am);
+        const int k = unit_exponent(am);
+        if (here == 0) p.e[row] = row_factor<kFmt>(p, row, k, finite);
+        if (here >= p.Ci) continue;
+        float v[8];
+        uint64_t v2[4];
+        values8<kFmt>(raw, v);
+        scaled_pairs(v, inv_scale(k), finite, v2);
+        uint8_t* dst = p.digits + (size_t)row * kDigits * (p.Ci / 2) + here / 2;
 #pragma unroll
-    for (int q = 0; q < kDigits; q++) *reinterpret_cast<uint32_t*>(dst + (size_t)q * (p.Ci / 2)) = next_digits8(v2);
+        for (int q = 0; q < kDigits; q++) *reinterpret_cast<uint32_t*>(dst + (size_t)q * (p.Ci / 2)) = next_digits8(v2);
+    }
 }
 
 // acc[n] += X L1 over the 64 channels of block b for 16 rows (or eight) and the ranks j0 + 8 n to + 7: lane t of a
@@ -418,15 +431,15 @@ __device__ __forceinline__ void lowrank_store(float* dst, int rank, int g, int t
     }
 }
 
-// U of 16 rows and 32 ranks by a cluster of eight CTAs, an eighth of the channels each: a warp takes 16 of the ranks
-// and one 64-channel block (every so manieth, past 8192 channels).  The sums are joined in rank order through distributed shared memory and
+// U of 16 rows and 32 ranks by a cluster of CTAs, a part of the channels each: a warp takes 16 of the ranks and one
+// 64-channel block with eight CTAs (every so manieth with fewer, and past 8192 channels).  The sums are joined in rank order through distributed shared memory and
 // kept as BF16 hi + lo, 2^-17 of the value.
 template <int kFmt>
 __device__ __forceinline__ void lowrank_cluster(const RowsParams& p, int index, float (*wpart)[16][32], float (*part)[32]) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int crank = (int)cluster_ctarank(), rgroups = (p.rank + 31) / 32;
     const int m0 = index / rgroups * 16, nm = imin(16, p.rows - m0), j0 = index % rgroups * 32;
-    const int nblk = p.Ci / 64, b0 = nblk * crank / kPrepCluster, b1 = nblk * (crank + 1) / kPrepCluster;
+    const int nblk = p.Ci / 64, csize = p.prep_cluster, sh = 31 - __clz(csize), b0 = nblk * crank >> sh, b1 = nblk * (crank + 1) >> sh;   // a power of two
     const int jw = j0 + 16 * (warp & 1), ks = warp >> 1, nks = (int)blockDim.x >> 6, warps = (int)blockDim.x >> 5;
     float acc[2][4] = {};
     if (jw < p.rank && ks < nks) {
@@ -445,22 +458,25 @@ __device__ __forceinline__ void lowrank_cluster(const RowsParams& p, int index, 
         part[m][lane] = u;
     }
     cluster_sync();
-    // an eighth of the sums per CTA: two rows
-    const int m = 2 * crank + (warp & 1), j = j0 + lane;
-    uint16_t* dst = p.u + (long long)(m0 + m) * p.slab;
-    if (warp < 2 && m < nm && j < p.rank) {
-        const uint32_t at = smem_u32(&part[m][lane]);
-        float v[kPrepCluster], u = 0.f;
+    // each CTA joins the sums of 16 / csize rows
+    const int per = 16 >> sh;
+    for (int i = warp; i < per; i += warps) {
+        const int m = crank * per + i, j = j0 + lane;
+        uint16_t* dst = p.u + (long long)(m0 + m) * p.slab;
+        if (m < nm && j < p.rank) {
+            const uint32_t at = smem_u32(&part[m][lane]);
+            float v[kPrepCluster], u = 0.f;
 #pragma unroll
-        for (int c = 0; c < kPrepCluster; c++) v[c] = ld_dsmem_f32(mapa_shared(at, c));
+            for (int c = 0; c < kPrepCluster; c++) v[c] = c < csize ? ld_dsmem_f32(mapa_shared(at, c)) : 0.f;
 #pragma unroll
-        for (int c = 0; c < kPrepCluster; c++) u += v[c];
-        if (kFmt == DQ_ROWS_E4M3) u *= p.x_scales[m0 + m];
-        const uint16_t hi = f32_to_bf16_rn(u);
-        dst[j] = hi;
-        dst[p.rank + j] = f32_to_bf16_rn(u - bf16_lo(hi));
-    } else if ((warp >> 1) == 1 && m < nm && j0 == 0 && 2 * p.rank + lane < p.slab) {
-        dst[2 * p.rank + lane] = 0;   // zeros up to the slab's width (at most 32 columns)
+            for (int c = 0; c < kPrepCluster; c++) u += v[c];
+            if (kFmt == DQ_ROWS_E4M3) u *= p.x_scales[m0 + m];
+            const uint16_t hi = f32_to_bf16_rn(u);
+            dst[j] = hi;
+            dst[p.rank + j] = f32_to_bf16_rn(u - bf16_lo(hi));
+        }
+        // zeros up to the slab's width (at most 32 columns)
+        if (m < nm && j0 == 0 && 2 * p.rank + lane < p.slab) dst[2 * p.rank + lane] = 0;
     }
     cluster_sync();   // no CTA leaves while another still reads its sums
 }
@@ -470,13 +486,12 @@ __global__ void __launch_bounds__(kPrepThreads) k_rows_prepare(RowsParams p) {
     griddep_wait();     // the launch before this one may still read the workspace, or write X
     __shared__ float wpart[16][16][32], part[16][32];
     // the low-rank clusters first: they take longest
-    const int parts = prep_parts(p.Ci), b = (int)blockIdx.x;
-    const int low = (p.rows + 15) / 16 * ((p.rank + 31) / 32) * kPrepCluster;
+    const int b = (int)blockIdx.x, low = (p.rows + 15) / 16 * ((p.rank + 31) / 32) * p.prep_cluster;
     if (b == 0 && threadIdx.x == 0) *p.status = header_ok(p) ? 0 : kStatusBadWeight;
     if (b < low)
-        lowrank_cluster<kFmt>(p, b / kPrepCluster, wpart, part);
-    else if (b - low < p.rows * parts)
-        digits_block<kFmt>(p, (b - low) / parts, (b - low) % parts);
+        lowrank_cluster<kFmt>(p, b / p.prep_cluster, wpart, part);
+    else
+        digits_blocks<kFmt>(p, b - low, (int)gridDim.x - low);
 }
 
 // ------------------------------------------------------------------ the product
@@ -998,6 +1013,27 @@ cudaError_t resident_clusters(int size, int* clusters) {
     return cudaSuccess;
 }
 
+// k_rows_prepare's clusters and CTAs (RowsParams' fields prep_*)
+cudaError_t prepare_plan(RowsParams& p) {
+    int sms = 0;
+    cudaError_t e = resident_clusters(1, &sms);
+    if (e != cudaSuccess) return e;
+    // A CTA per row's piece and clusters of eight, while they are no more than four times what fits at once (64
+    // registers a thread); else as many CTAs as fit, half of them low-rank ones at most, in smaller clusters, and
+    // the others take piece after piece.  5120 -> 5120: 256 rows 42.1 us either way, 512 rows 71 us against 62 us;
+    // 256 rows 5120 -> 13824: 76.5 us against 79 us.
+    const long long fit = (long long)sms * (1024 / prep_threads(p.Ci)), groups = cdiv(p.rows, 16) * cdiv(p.rank, 32);
+    long long pieces = (long long)p.rows * prep_parts(p.Ci);
+    p.prep_cluster = kPrepCluster;
+    if (groups * kPrepCluster + pieces > 4 * fit) {
+        while (p.prep_cluster > 1 && groups * p.prep_cluster > fit / 2) p.prep_cluster /= 2;
+        const long long rest = fit - groups * p.prep_cluster, most = rest >= fit / 4 ? rest : fit;
+        if (pieces > most) pieces = most;
+    }
+    p.prep_ctas = (groups + cdiv(pieces, p.prep_cluster)) * p.prep_cluster;
+    return cudaSuccess;
+}
+
 }  // namespace
 
 // How the product of `rows` rows is cut (RowsParams' fields from n_rows on).
@@ -1039,7 +1075,7 @@ cudaError_t rows_plan(RowsParams& p) {
         if (own && (p.stages < imin(6, p.own_stages) || p.own_stages > own_turns(p.rows) * own_warps(p.rows))) continue;
         break;
     }
-    return cudaSuccess;
+    return p.own_digits ? cudaSuccess : prepare_plan(p);
 }
 
 cudaError_t launch_rows(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const CUtensorMap& tm_x, const CUtensorMap& tm_l2,
@@ -1062,10 +1098,9 @@ cudaError_t launch_rows(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const 
                 return cudaFuncSetAttribute(prepare, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
             });
             if (e != cudaSuccess) return e;
-            const long long blocks = cdiv((long long)p.rows * prep_parts(p.Ci), kPrepCluster);
-            attr[1].val.clusterDim.x = kPrepCluster;
+            attr[1].val.clusterDim.x = (unsigned)p.prep_cluster;
             attr[1].val.clusterDim.y = 1;
-            cfg.gridDim = dim3((unsigned)((blocks + cdiv(p.rows, 16) * cdiv(p.rank, 32)) * kPrepCluster));
+            cfg.gridDim = dim3((unsigned)p.prep_ctas);
             cfg.blockDim = dim3((unsigned)prep_threads(p.Ci));
             if ((e = cudaLaunchKernelEx(&cfg, prepare, p)) != cudaSuccess) return e;
         }
