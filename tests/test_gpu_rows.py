@@ -391,6 +391,17 @@ def test_few_rows_of_every_count(dq, Ci, Co, rank, rows):
         assert_within(run_rows(dq, dev, w, x, sc, fmt, gelu=fmt == 2, y_pad=rows % 2), ref, tol, "Y")
 
 
+@pytest.mark.parametrize("Ci,Co,rank,rows", [(256, 20480, 16, 9), (256, 20480, 112, 17), (512, 20480, 32, 64), (256, 5120, 128, 130),
+                                             (768, 5120, 48, 155), (1280, 5120, 64, 310), (512, 2560, 32, 1001), (256, 256, 16, 4740)])
+def test_rows_with_more_work_than_fits_at_once(dq, Ci, Co, rank, rows):
+    """Layers of many tiles and many rows, odd counts of them in a pass."""
+    w, dev = weight(dq, Ci, Co, rank, seed=Ci + Co, bias=True)
+    for fmt in (0, 1, 2):
+        v, x, sc = rows_input(rows, Ci, fmt, seed=rows + fmt)
+        ref, tol = rows_reference(w, v, fmt == 1)
+        assert_within(run_rows(dq, dev, w, x, sc, fmt, gelu=fmt == 1, x_pad=16, y_pad=3), ref, tol, "Y")
+
+
 @pytest.mark.parametrize("rows", [4, 40])
 def test_rows_with_scales_that_are_not_finite(dq, rows):
     w, dev = weight(dq, 512, 768, 32, seed=512)

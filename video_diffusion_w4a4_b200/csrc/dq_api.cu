@@ -925,10 +925,10 @@ int dq_rows_forward(const void* X, int x_format, long long x_stride, const float
     if (p.own_digits) {
         tm_x = tm_l2 = tm_u = tm_w;   // not read
     } else {
-        if (!map_2d(&tm_x, p.digits, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Ci / 2, (uint64_t)rows * 8, 128, p.n_pad))
+        if (!map_2d(&tm_x, p.digits, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Ci / 2, (uint64_t)rows * 8, 128, p.pairs ? p.n_pad / 2 : p.n_pad))
             return map_fail("digits");
         if (!map_2d(&tm_l2, L2_slab, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pl.slab, Co, 64, 128)) return map_fail("L2");
-        if (!map_2d(&tm_u, p.u, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pl.slab, rows, 64, (uint32_t)dq::cdiv(p.n_rows, 16) * 16))
+        if (!map_2d(&tm_u, p.u, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pl.slab, rows, 64, (uint32_t)dq::cdiv(p.n_rows, 16) * (p.pairs ? 8 : 16)))
             return map_fail("U");
     }
     e = dq::launch_rows(tm_w, tm_s, tm_x, tm_l2, tm_u, p, (cudaStream_t)stream);

@@ -141,6 +141,7 @@ struct RowsParams {
     int n_rows, n_pad, passes;  // rows of X per pass, their digits' columns
     int splits, group;          // parts of the channels, and tiles, of a cluster
     int stages, d_cols;
+    int pairs, pair_ctas;       // by CTA pairs, so many at once
     int own_digits, own_stages; // the product writes the digits itself (of up to so many 256-channel stages), and U L2
     int u_parts;                //   parts of a CTA's channels of U
     int prep_cluster;           // else k_rows_prepare's CTAs

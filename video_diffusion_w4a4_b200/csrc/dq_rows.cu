@@ -137,6 +137,20 @@ __device__ __forceinline__ void tmem_cp_32x128b(uint32_t taddr, uint64_t sdesc) 
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
+// ... in both CTAs of a pair, each from its own shared memory to its own tensor memory
+__device__ __forceinline__ void tmem_cp_pair_32x128b(uint32_t taddr, uint64_t sdesc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* map, uint32_t bar_cluster, int x, int y, int z,
+                                                 int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(bar_cluster), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
 __device__ __forceinline__ void mma_nvfp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
                                           uint32_t sfb, uint32_t accumulate) {
     asm volatile(
@@ -510,12 +524,20 @@ struct Ring {
 };
 
 struct Bars {
-    uint64_t full[kStages], empty[kStages], accf, digits[kOwnTurns], u;
-    float e[kPassRows];   // the rows' factors
+    uint64_t full[kStages], empty[kStages], accf, acce, digits[kOwnTurns], u;
+    float e[2][kPassRows];   // the rows' factors
     float amax[8];        // own digits: each warp's part of its row's largest magnitude
     uint32_t tmem;
     int abort_flag;
 };
+
+// The digits' scales: E4M3 1 in eight columns of the warp's lanes
+__device__ __forceinline__ void ones(uint32_t taddr) {
+    const uint32_t one = 0x38383838u;
+    tmem_st_x4(taddr, one, one, one, one);
+    tmem_st_x4(taddr + 4, one, one, one, one);
+    tmem_st_wait();
+}
 
 // Own digits: the epilogue warps write the digits of this CTA's channels into shared memory as the MMA reads
 // them, with the unit of the rows' values in these channels alone.  Each row takes own_warps(rows) warps, which
@@ -549,7 +571,7 @@ __device__ __forceinline__ void write_own_digits(const RowsParams& p, Bars& bars
     for (int i = 0; i < per; i++) am = max_nan(am, bars.amax[m * per + i]);
     const bool finite = finite_row(am);
     const int k = unit_exponent(am);
-    if (m < p.rows && part == 0 && lane == 0) bars.e[m] = row_factor<kFmt>(p, m, k, finite);
+    if (m < p.rows && part == 0 && lane == 0) bars.e[0][m] = row_factor<kFmt>(p, m, k, finite);
     const Scale2 s = inv_scale(k);
 #pragma unroll
     for (int i = 0; i < kOwnTurns; i++) {
@@ -652,8 +674,12 @@ __device__ __forceinline__ void lowrank_term(const RowsParams& p, Bars& bars, fl
     bar_arrive(5, 512);   // the epilogue warps wait for it
 }
 
-template <int kFmt, bool kOwn>
-__global__ void __launch_bounds__(product_threads(kOwn), 1)
+// The product's forms: from prepared rows, from rows whose digits it writes itself, and from prepared rows by CTA pairs
+// (two tiles of output channels, each CTA with half of the digits' columns in its shared memory).
+enum { kPrepared = 0, kOwnDigits = 1, kPairs = 2 };
+
+template <int kFmt, int kForm>
+__global__ void __launch_bounds__(product_threads(kForm == kOwnDigits), 1)
     k_rows_product(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_s,
                    const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_l2,
                    const __grid_constant__ CUtensorMap tm_u, RowsParams p) {
@@ -662,14 +688,17 @@ __global__ void __launch_bounds__(product_threads(kOwn), 1)
     __shared__ Bars bars;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int S = p.stages;
-    constexpr bool own = kOwn;
-    const int split = (int)blockIdx.x, splits = (int)gridDim.x;       // parts of the channels
+    constexpr bool own = kForm == kOwnDigits, pairs = kForm == kPairs;
+    const int split = pairs ? 0 : (int)blockIdx.x, splits = pairs ? 1 : (int)gridDim.x;   // parts of the channels
     const int csize = splits * p.group, crank = (int)cluster_ctarank();   // in the cluster: those of `group` tiles
-    const int o0 = (int)blockIdx.y * 128;
-    const int m0 = (int)blockIdx.z * p.n_rows;
-    const int nm = imin(p.n_rows, p.rows - m0);
+    // a CTA's work: one tile of output channels and one pass over rows; pairs take one such piece after another
+    const int tiles = p.Co / 256, item0 = pairs ? (int)blockIdx.y : 0, items = pairs ? tiles * p.passes : 1,
+              step = pairs ? (int)gridDim.y : 1;
+    auto tile_of = [&](int item) { return pairs ? (item % tiles * 2 + crank) * 128 : (int)blockIdx.y * 128; };
+    auto rows_of = [&](int item) { return (pairs ? item / tiles : (int)blockIdx.z) * p.n_rows; };
+    int o0 = tile_of(item0), m0 = rows_of(item0), nm = imin(p.n_rows, p.rows - m0);   // the epilogue's piece at hand
     const int k256 = p.Ci / 256, a0 = k256 * split / splits, nA = k256 * (split + 1) / splits - a0;
-    const uint32_t b_all = (uint32_t)p.n_pad * 128u, b_bytes = own ? 0u : b_all;   // digits of a stage; those in the ring
+    const uint32_t b_all = (uint32_t)p.n_pad * (pairs ? 64u : 128u), b_bytes = own ? 0u : b_all;   // digits of a stage; those in the ring
     const uint32_t stage = kCodeBytes + b_bytes + kScaleBytes;        // codes, digits, the codes' scales
     uint8_t* digits = sm + (size_t)S * stage;                         // own digits: [stage][column][128 bytes]
     const int total = nA + (!own && split == 0 ? p.slab / 64 : 0);    // stages: the weight's, then the low-rank factor's
@@ -687,12 +716,18 @@ __global__ void __launch_bounds__(product_threads(kOwn), 1)
         for (int i = 0; i < kOwnTurns; i++) mbar_init(&bars.digits[i], kEpiThreads / 32);
         mbar_init(&bars.u, (uint32_t)csize);
         mbar_init(&bars.accf, 1);
+        mbar_init(&bars.acce, 2 * kEpiThreads / 32);
         bars.abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
-        tmem_alloc(&bars.tmem, kTmemCols);
-        tmem_relinquish();
+        if (pairs) {
+            tmem_alloc_pair(&bars.tmem, kTmemCols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(&bars.tmem, kTmemCols);
+            tmem_relinquish();
+        }
     }
     if (warp == 0 && lane == 0) {
         prefetch_tmap(&tm_w);
@@ -704,7 +739,11 @@ __global__ void __launch_bounds__(product_threads(kOwn), 1)
         }
     }
     tc_fence_before();
-    __syncthreads();
+    __syncwarp();
+    if (pairs)
+        cluster_sync();   // both CTAs' barriers are initialised
+    else
+        __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars.tmem, t_low = tmem + (uint32_t)p.d_cols, t_one = t_low + n16, t_sf = t_one + 8;
     if (own) {
@@ -712,30 +751,51 @@ __global__ void __launch_bounds__(product_threads(kOwn), 1)
         griddep_wait();     // with k_rows_prepare in front everything before that launch is done already
     }
     griddep_launch();
+    const bool lead = !pairs || crank == 0;   // the CTA that issues the MMAs, and has the stages' full barriers
+    if (pairs) {
+        if (warp >= 4 && warp < 8) ones(t_one + ((uint32_t)((warp & 3) * 32) << 16));
+        tc_fence_before();
+        __syncwarp();
+        cluster_sync();
+        tc_fence_after();
+    }
 
     if (warp == 0) {
         // ------------------------------------------------ codes and their scales
         if (own) bar_sync(3, 32 + 512);   // the loads of everything else are under way
         if (lane == 0) {
-            const int half = (o0 >> 7) & 1, blk0 = (o0 >> 8) * (p.Ci / 64) + a0 * 4;
             Ring r;
-            int g = 0;
-            for (; g < total; g++, r.next(S)) {
-                uint64_t* full = &bars.full[r.slot];
-                if (g >= S && !mbar_wait(&bars.empty[r.slot], r.phase ^ 1, abort_flag, p.status, p.budget_ns)) break;
-                uint8_t* dst = sm + (size_t)r.slot * stage;
-                if (g < nA) {
-                    mbar_arrive_expect_tx(full, kCodeBytes + kScaleBytes);
-                    tma_load_2d(dst, &tm_w, full, (a0 + g) * 128, o0);
-                    // 32 lanes x 16 bytes per 64-channel block: one half of the 256-row tile
-                    tma_load_4d(dst + kCodeBytes + b_bytes, &tm_s, full, 0, half, 0, blk0 + 4 * g);
-                } else {
-                    mbar_arrive_expect_tx(full, kCodeBytes);
-                    tma_load_2d(dst, &tm_l2, full, (g - nA) * 64, o0);
+            int n = 0;   // stages so far
+            bool ok = true;
+            for (int item = item0; item < items && ok; item += step) {
+                const int o = tile_of(item), half = (o >> 7) & 1, blk0 = (o >> 8) * (p.Ci / 64) + a0 * 4;
+                for (int g = 0; g < total; g++, n++, r.next(S)) {
+                    uint64_t* full = &bars.full[r.slot];
+                    if (n >= S && !(ok = mbar_wait(&bars.empty[r.slot], r.phase ^ 1, abort_flag, p.status, p.budget_ns))) break;
+                    uint8_t* dst = sm + (size_t)r.slot * stage;
+                    if (pairs) {
+                        if (lead) mbar_arrive_expect_tx(full, 2 * (g < nA ? kCodeBytes + kScaleBytes : kCodeBytes));
+                        const uint32_t at = mapa_shared(smem_u32(full), 0);
+                        if (g < nA) {
+                            tma_load_2d_pair(dst, &tm_w, at, (a0 + g) * 128, o);
+                            tma_load_4d_pair(dst + kCodeBytes + b_bytes, &tm_s, at, 0, half, 0, blk0 + 4 * g);
+                        } else {
+                            tma_load_2d_pair(dst, &tm_l2, at, (g - nA) * 64, o);
+                        }
+                    } else if (g < nA) {
+                        mbar_arrive_expect_tx(full, kCodeBytes + kScaleBytes);
+                        tma_load_2d(dst, &tm_w, full, (a0 + g) * 128, o);
+                        // 32 lanes x 16 bytes per 64-channel block: one half of the 256-row tile
+                        tma_load_4d(dst + kCodeBytes + b_bytes, &tm_s, full, 0, half, 0, blk0 + 4 * g);
+                    } else {
+                        mbar_arrive_expect_tx(full, kCodeBytes);
+                        tma_load_2d(dst, &tm_l2, full, (g - nA) * 64, o);
+                    }
                 }
             }
-            for (int q = g > S ? g - S : 0; q < g; q++)   // every copy lands before shared memory is released
-                mbar_wait(&bars.full[q % S], (uint32_t)(q / S) & 1, abort_flag, nullptr, p.budget_ns, false);
+            // every copy lands before shared memory is released (a pair's second CTA: the MMAs have read them)
+            for (int q = n > S ? n - S : 0; q < n; q++)
+                mbar_wait(lead ? &bars.full[q % S] : &bars.empty[q % S], (uint32_t)(q / S) & 1, abort_flag, nullptr, p.budget_ns, !lead);
         }
         __syncwarp();
     } else if (warp == 2) {
@@ -743,75 +803,105 @@ __global__ void __launch_bounds__(product_threads(kOwn), 1)
         if (lane == 0 && !own) {
             griddep_wait();
             Ring r;
-            int g = 0;
-            for (; g < total; g++, r.next(S)) {
-                uint64_t* full = &bars.full[r.slot];
-                if (g >= S && !mbar_wait(&bars.empty[r.slot], r.phase ^ 1, abort_flag, p.status, p.budget_ns)) break;
-                uint8_t* dst = sm + (size_t)r.slot * stage + kCodeBytes;
-                mbar_arrive_expect_tx(full, g < nA ? b_bytes : n16 * 128);   // U within the digits' and scales' places
-                if (g < nA)
-                    tma_load_2d(dst, &tm_x, full, (a0 + g) * 128, m0 * kDigits);
-                else
-                    tma_load_2d(dst, &tm_u, full, (g - nA) * 64, m0);
+            int n = 0;
+            bool ok = true;
+            for (int item = item0; item < items && ok; item += step) {
+                const int m = rows_of(item);
+                for (int g = 0; g < total; g++, n++, r.next(S)) {
+                    uint64_t* full = &bars.full[r.slot];
+                    if (n >= S && !(ok = mbar_wait(&bars.empty[r.slot], r.phase ^ 1, abort_flag, p.status, p.budget_ns))) break;
+                    uint8_t* dst = sm + (size_t)r.slot * stage + kCodeBytes;
+                    if (lead) mbar_arrive_expect_tx(full, g < nA ? (pairs ? 2 : 1) * b_bytes : n16 * 128);   // U in the digits' place
+                    if (pairs) {
+                        const uint32_t at = mapa_shared(smem_u32(full), 0);
+                        if (g < nA)
+                            tma_load_2d_pair(dst, &tm_x, at, (a0 + g) * 128, m * kDigits + crank * (p.n_pad / 2));
+                        else
+                            tma_load_2d_pair(dst, &tm_u, at, (g - nA) * 64, m + crank * (int)(n16 / 2));
+                    } else if (g < nA) {
+                        tma_load_2d(dst, &tm_x, full, (a0 + g) * 128, m * kDigits);
+                    } else {
+                        tma_load_2d(dst, &tm_u, full, (g - nA) * 64, m);
+                    }
+                }
             }
-            for (int q = g > S ? g - S : 0; q < g; q++)
-                mbar_wait(&bars.full[q % S], (uint32_t)(q / S) & 1, abort_flag, nullptr, p.budget_ns, false);
+            for (int q = n > S ? n - S : 0; q < n; q++)
+                mbar_wait(lead ? &bars.full[q % S] : &bars.empty[q % S], (uint32_t)(q / S) & 1, abort_flag, nullptr, p.budget_ns, !lead);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ MMAs, by one lane throughout
-        bar_sync(2, 32 + 128);   // the digits' scales are in tensor memory
+        if (!pairs) bar_sync(2, 32 + 128);   // the digits' scales are in tensor memory
         tc_fence_after();
-        if (elect_one()) {
-            const uint32_t idesc = idesc_nvfp4(128, p.n_pad), id_low = idesc_bf16(128, (int)n16);
+        if (lead && elect_one()) {
+            constexpr int M = pairs ? 256 : 128;
+            const uint32_t idesc = idesc_nvfp4(M, p.n_pad), id_low = idesc_bf16(M, (int)n16);
             // descriptors: the address field is the offset / 16, so a step is an addition
-            const uint32_t base = smem_u32(sm), step = stage >> 4, b_step = own ? b_all >> 4 : step;
+            const uint32_t base = smem_u32(sm), step16 = stage >> 4, b_step = own ? b_all >> 4 : step16;
             const uint64_t a0d = desc_k_sw128(base), b0d = desc_k_sw128(own ? smem_u32(digits) : base + kCodeBytes),
                            f0d = smem_desc(base + kCodeBytes + b_bytes, 128, 128, 0);
+            auto commit = [](uint64_t* bar) {
+                if (pairs)
+                    tc_commit_pair_both(bar, 3);
+                else
+                    tc_commit(bar);
+            };
             Ring r;
             uint64_t ad = a0d, bd = b0d, fd = f0d;
-            uint32_t ta = t_sf, more = 0;
-            int turn = 0, left = 0, g = 0;                   // own digits: stages until the next turn's barrier
+            uint32_t ta = t_sf, used = 0;                    // pieces so far
+            int turn = 0, left = 0;                          // own digits: stages until the next turn's barrier
             const int per = own_warps(p.rows);
-            for (; g < nA; g++) {
-                if (own && left-- == 0) {
-                    if (!mbar_wait_spin(&bars.digits[turn], 0, abort_flag, p.status, p.budget_ns)) break;
-                    turn++;
-                    left = per - 1;
-                }
-                if (!mbar_wait_spin(&bars.full[r.slot], r.phase, abort_flag, p.status, p.budget_ns)) break;
+            bool ok = true;
+            for (int item = item0; item < items && ok; item += step, used++) {
+                if (used && !mbar_wait_spin(&bars.acce, (used - 1) & 1, abort_flag, p.status, p.budget_ns)) break;
                 tc_fence_after();
-                // the stage's own columns: nothing still reads them, as its empty barrier was waited for
-#pragma unroll
-                for (int j = 0; j < 4; j++) tmem_cp_32x128b(ta + 4 * j, fd + 32 * j);
-                mma_nvfp4(tmem, ad, bd, idesc, ta, t_one, more);
-                more = 1;
-#pragma unroll
-                for (int j = 1; j < 4; j++) mma_nvfp4(tmem, ad + 2 * j, bd + 2 * j, idesc, ta + 4 * j, t_one, 1u);
-                tc_commit(&bars.empty[r.slot]);
-                ad += step, bd += b_step, fd += step, ta += 16;
-                r.next(S);
-                if (r.slot == 0) {
-                    ad = a0d, fd = f0d, ta = t_sf;
-                    if (!own) bd = b0d;
-                }
-            }
-            if (!own && g == nA) {
-                more = 0;
-                for (; g < total; g++) {
-                    if (!mbar_wait_spin(&bars.full[r.slot], r.phase, abort_flag, p.status, p.budget_ns)) break;
+                uint32_t more = 0;
+                for (int g = 0; g < total; g++) {
+                    if (own && left-- == 0) {
+                        if (!(ok = mbar_wait_spin(&bars.digits[turn], 0, abort_flag, p.status, p.budget_ns))) break;
+                        turn++;
+                        left = per - 1;
+                    }
+                    if (!(ok = mbar_wait_spin(&bars.full[r.slot], r.phase, abort_flag, p.status, p.budget_ns))) break;
                     tc_fence_after();
+                    if (own || g < nA) {
+                        // the stage's own columns: nothing still reads them, as its empty barrier was waited for
 #pragma unroll
-                    for (int j = 0; j < 4; j++) mma_bf16(t_low, ad + 2 * j, bd + 2 * j, id_low, more | (uint32_t)j);
-                    more = 1;
-                    tc_commit(&bars.empty[r.slot]);
-                    ad += step, bd += step;
+                        for (int j = 0; j < 4; j++) {
+                            if (pairs)
+                                tmem_cp_pair_32x128b(ta + 4 * j, fd + 32 * j);
+                            else
+                                tmem_cp_32x128b(ta + 4 * j, fd + 32 * j);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            if (pairs)
+                                mma_nvfp4_pair(tmem, ad + 2 * j, bd + 2 * j, idesc, ta + 4 * j, t_one, j ? 1u : more);
+                            else
+                                mma_nvfp4(tmem, ad + 2 * j, bd + 2 * j, idesc, ta + 4 * j, t_one, j ? 1u : more);
+                        }
+                        more = g + 1 != nA;   // the low-rank factor's steps have columns of their own
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            if (pairs)
+                                mma_bf16_pair(t_low, ad + 2 * j, bd + 2 * j, id_low, more | (uint32_t)j);
+                            else
+                                mma_bf16(t_low, ad + 2 * j, bd + 2 * j, id_low, more | (uint32_t)j);
+                        }
+                        more = 1;
+                    }
+                    commit(&bars.empty[r.slot]);
+                    ad += step16, bd += b_step, fd += step16, ta += 16;
                     r.next(S);
-                    if (r.slot == 0) ad = a0d, bd = b0d;
+                    if (r.slot == 0) {
+                        ad = a0d, fd = f0d, ta = t_sf;
+                        if (!own) bd = b0d;
+                    }
                 }
+                commit(&bars.accf);
             }
-            tc_commit(&bars.accf);
-            mbar_wait(&bars.accf, 0, abort_flag, nullptr, p.budget_ns, false);   // no MMA runs past this point
+            if (used) mbar_wait(&bars.accf, (used - 1) & 1, abort_flag, nullptr, p.budget_ns, false);   // no MMA runs past this point
         }
         __syncwarp();
     }
@@ -834,12 +924,8 @@ __global__ void __launch_bounds__(product_threads(kOwn), 1)
         bias = *(const float*)(p.packed_w + p.off_bias + 4ll * (o0 + row));
         S_W = hdr->S_W;
         if (own) bar_arrive(3, 32 + 512);   // the weight may follow
-        if (warp < 8) {
-            // the digits' scales: E4M3 1 in eight columns of every lane
-            const uint32_t one = 0x38383838u;
-            tmem_st_x4(t_one + trow, one, one, one, one);
-            tmem_st_x4(t_one + trow + 4, one, one, one, one);
-            tmem_st_wait();
+        if (!pairs && warp < 8) {
+            ones(t_one + trow);
             tc_fence_before();
             __syncwarp();
             bar_arrive(2, 32 + 128);
@@ -849,17 +935,20 @@ __global__ void __launch_bounds__(product_threads(kOwn), 1)
             cluster_wait();
         } else {
             griddep_wait();   // the rows' factors come from k_rows_prepare
-            if (et < nm) bars.e[et] = p.e[m0 + et];
+            if (!pairs && et < nm) bars.e[0][et] = p.e[m0 + et];
         }
-        bar_sync(1, kEpiThreads);
         ok = header_ok(p);
-        if (own) bar_sync(5, 512);   // the low-rank term
-        if (lane == 0) done = mbar_wait(&bars.accf, 0, abort_flag, p.status, p.budget_ns);
-        done = __shfl_sync(0xffffffffu, done, 0);
-        tc_fence_after();
+        if (!pairs) {
+            bar_sync(1, kEpiThreads);
+            if (own) bar_sync(5, 512);   // the low-rank term
+            if (lane == 0) done = mbar_wait(&bars.accf, 0, abort_flag, p.status, p.budget_ns);
+            done = __shfl_sync(0xffffffffu, done, 0);
+            tc_fence_after();
+        }
     }
     if (own && tid == 96 && blockIdx.x + blockIdx.y + blockIdx.z == 0) *p.status = header_ok(p) ? 0 : kStatusBadWeight;
-    const float bv = (flags & kPackedHasBias) ? bias : 0.f;
+    float bv = (flags & kPackedHasBias) ? bias : 0.f;
+    uint32_t used = 0;   // pieces so far
     // This CTA's part of the rows 4 b to 4 b + 3 for the thread's output channel: the digits' columns with
     // weights 8^-p, times S_W and the row's factor, and U L2 where this CTA has it
     auto parts_of = [&](int b, float (&v)[4]) {
@@ -873,12 +962,12 @@ __global__ void __launch_bounds__(product_threads(kOwn), 1)
             v[i] = __uint_as_float(acc[kDigits * i + kDigits - 1]);
 #pragma unroll
             for (int q = kDigits - 2; q >= 0; q--) v[i] = fmaf(v[i], 0.125f, __uint_as_float(acc[kDigits * i + q]));
-            v[i] = fmaf(v[i] * S_W, bars.e[imin(4 * b + i, nm - 1)], !own && split == 0 ? __uint_as_float(low[i]) : 0.f);
+            v[i] = fmaf(v[i] * S_W, bars.e[used & 1][imin(4 * b + i, nm - 1)], !own && split == 0 ? __uint_as_float(low[i]) : 0.f);
         }
     };
     // Y of the thread's output channel for the i-th of the rows split, split + splits, ... that this CTA finishes, and
     // for the next where there is one
-    const int mine = split < nm ? (nm - split + splits - 1) / splits : 0;
+    int mine = split < nm ? (nm - split + splits - 1) / splits : 0;
     auto finish = [&](int i, float y0, float y1) {
         const int m = split + i * splits;
         const bool two = i + 1 < mine;
@@ -889,7 +978,35 @@ __global__ void __launch_bounds__(product_threads(kOwn), 1)
         dst[0] = f32_to_bf16_rn(y0);
         if (two) dst[(long long)splits * p.y_stride] = f32_to_bf16_rn(y1);
     };
-    if (splits == 1) {
+    if (pairs) {
+        for (int item = item0; item < items && epi; item += step, used++) {
+            o0 = tile_of(item), m0 = rows_of(item), mine = nm = imin(p.n_rows, p.rows - m0);
+            if (used && (flags & kPackedHasBias)) bv = *(const float*)(p.packed_w + p.off_bias + 4ll * (o0 + row));
+            if (et < nm) bars.e[used & 1][et] = p.e[m0 + et];
+            bar_sync(1, kEpiThreads);
+            // (a warp whose wait has run out goes on without writing, as the others still meet it at the barrier)
+            bool full = true;
+            if (lane == 0) full = mbar_wait(&bars.accf, used & 1, abort_flag, p.status, p.budget_ns);
+            done = __shfl_sync(0xffffffffu, full, 0) && done;
+            tc_fence_after();
+            float v[kPassRows / 8][4];
+#pragma unroll
+            for (int k = 0; k < kPassRows / 8; k++)
+                if (4 * (group + 2 * k) < nm) parts_of(group + 2 * k, v[k]);
+            // the accumulator is free for the next piece
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bars.acce), 0));
+#pragma unroll
+            for (int k = 0; k < kPassRows / 8; k++) {
+                const int b = group + 2 * k;
+                if (4 * b < nm && done && ok) {
+                    finish(4 * b, v[k][0], v[k][1]);
+                    if (4 * b + 2 < nm) finish(4 * b + 2, v[k][2], v[k][3]);
+                }
+            }
+        }
+    } else if (splits == 1) {
         if (epi && done && ok) {
             for (int b = group; 4 * b < nm; b += 2) {
                 float v[4];
@@ -934,10 +1051,17 @@ __global__ void __launch_bounds__(product_threads(kOwn), 1)
         }
     }
     tc_fence_before();
-    __syncthreads();
+    __syncwarp();
+    if (pairs)
+        cluster_sync();   // neither CTA leaves while the other may still touch its shared memory or barriers
+    else
+        __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        if (pairs)
+            tmem_dealloc_pair(tmem, kTmemCols);
+        else
+            tmem_dealloc(tmem, kTmemCols);
     }
 }
 
@@ -966,16 +1090,18 @@ cudaError_t once_per_device(const void* kernel, Set set) {
 }
 
 // A call's two kernels; the product reads rows itself only when it writes their digits.
+template <int kFmt, typename F>
+auto by_form(const RowsParams& p, F f) {
+    return p.own_digits ? f(k_rows_prepare<kFmt>, k_rows_product<kFmt, kOwnDigits>)
+           : p.pairs    ? f(k_rows_prepare<kFmt>, k_rows_product<0, kPairs>)
+                        : f(k_rows_prepare<kFmt>, k_rows_product<0, kPrepared>);
+}
+
 template <typename F>
-auto by_format(int x_format, bool own, F f) {
-    if (x_format == DQ_ROWS_BF16)
-        return own ? f(k_rows_prepare<DQ_ROWS_BF16>, k_rows_product<DQ_ROWS_BF16, true>)
-                   : f(k_rows_prepare<DQ_ROWS_BF16>, k_rows_product<0, false>);
-    if (x_format == DQ_ROWS_E4M3)
-        return own ? f(k_rows_prepare<DQ_ROWS_E4M3>, k_rows_product<DQ_ROWS_E4M3, true>)
-                   : f(k_rows_prepare<DQ_ROWS_E4M3>, k_rows_product<0, false>);
-    return own ? f(k_rows_prepare<DQ_ROWS_E4M3_GROUP64>, k_rows_product<DQ_ROWS_E4M3_GROUP64, true>)
-               : f(k_rows_prepare<DQ_ROWS_E4M3_GROUP64>, k_rows_product<0, false>);
+auto by_format(const RowsParams& p, F f) {
+    return p.x_format == DQ_ROWS_BF16   ? by_form<DQ_ROWS_BF16>(p, f)
+           : p.x_format == DQ_ROWS_E4M3 ? by_form<DQ_ROWS_E4M3>(p, f)
+                                        : by_form<DQ_ROWS_E4M3_GROUP64>(p, f);
 }
 
 template <typename K>
@@ -996,7 +1122,7 @@ cudaError_t resident_clusters(int size, int* clusters) {
     if (dev >= kDevices) return cudaErrorInvalidDevice;
     std::atomic<int>& k = known[dev][size];
     if ((*clusters = k.load(std::memory_order_relaxed)) > 0) return cudaSuccess;
-    auto kernel = k_rows_product<0, false>;
+    auto kernel = k_rows_product<0, kPrepared>;
     if ((e = allow_smem(kernel)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -1043,7 +1169,8 @@ cudaError_t rows_plan(RowsParams& p) {
     p.passes = (int)cdiv(p.rows, p.n_rows);
     p.n_pad = p.n_rows * kDigits;
     p.d_cols = (int)cdiv(p.n_pad, 32) * 32;
-    const int tiles = p.Co / 128, k256 = p.Ci / 256, digits = p.n_pad * 128;
+    const int tiles = p.Co / 128, k256 = p.Ci / 256;
+    p.pairs = 0;
     for (int attempt = p.rows <= kOwnRows ? 0 : 1; attempt < 2; attempt++) {
         // up to kOwnRows rows the product does everything, if the digits and a ring of enough stages fit
         const bool own = attempt == 0;
@@ -1062,10 +1189,31 @@ cudaError_t rows_plan(RowsParams& p) {
             }
             if (p.group) break;
         }
+        if (!own && !p.group && p.passes > 2) {
+            // more work than CTAs fit at once: CTA pairs that take piece after piece, the next one's operands under way
+            // beside this one's output.  The passes (an even number of rows each: every CTA has half of the columns,
+            // 64 of them to a kilobyte-aligned place) are cut so that the longest pair's rows are fewest.  With one or
+            // two passes the weight's stream is the bound, which single CTAs keep up better: 5120 -> 13824, 48 rows
+            // 30 us by pairs, 25 us by single CTAs; 96 rows (three passes) 31 us against 36 us; 5120 -> 5120, 512 rows
+            // 57 us against 61 us (single CTAs, or pairs with one piece each: 63 us), 4096 rows 385 us against 440 us.
+            p.pairs = 1, p.group = 2;
+            int fit = 0;
+            cudaError_t e = resident_clusters(2, &fit);
+            if (e != cudaSuccess) return e;
+            long long best = 0;
+            for (int more = 0, least = p.passes; more < 4; more++) {
+                const int n = ((int)cdiv(p.rows, least + more) + 1) & ~1, passes = (int)cdiv(p.rows, n);
+                const long long longest = cdiv((long long)tiles / 2 * passes, fit) * n;
+                if (more == 0 || longest < best) best = longest, p.n_rows = n, p.passes = passes;
+            }
+            p.pair_ctas = imin(fit, tiles / 2 * p.passes);
+            p.n_pad = p.n_rows * kDigits;
+            p.d_cols = (int)cdiv(p.n_pad, 32) * 32;
+        }
         if (!p.group)   // more tiles than that: clusters of up to four of them for L1's sake
             for (p.group = own ? 4 : 1; tiles % p.group; p.group--) {
             }
-        const int items = p.rank / 16;
+        const int items = p.rank / 16, digits = p.n_pad * (p.pairs ? 64 : 128);
         p.u_parts = items < 8 ? 8 / items : 1;
         p.own_digits = own;
         p.own_stages = (int)cdiv(k256, p.splits);
@@ -1080,7 +1228,7 @@ cudaError_t rows_plan(RowsParams& p) {
 
 cudaError_t launch_rows(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const CUtensorMap& tm_x, const CUtensorMap& tm_l2,
                         const CUtensorMap& tm_u, const RowsParams& p, cudaStream_t st) {
-    return by_format(p.x_format, p.own_digits != 0, [&](auto prepare, auto product) {
+    return by_format(p, [&](auto prepare, auto product) {
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1105,9 +1253,15 @@ cudaError_t launch_rows(const CUtensorMap& tm_w, const CUtensorMap& tm_s, const 
             if ((e = cudaLaunchKernelEx(&cfg, prepare, p)) != cudaSuccess) return e;
         }
         if ((e = allow_smem(product)) != cudaSuccess) return e;
-        attr[1].val.clusterDim.x = (unsigned)p.splits;
-        attr[1].val.clusterDim.y = (unsigned)p.group;
-        cfg.gridDim = dim3((unsigned)p.splits, (unsigned)(p.Co / 128), (unsigned)p.passes);
+        if (p.pairs) {   // along x
+            attr[1].val.clusterDim.x = 2;
+            attr[1].val.clusterDim.y = 1;
+            cfg.gridDim = dim3(2, (unsigned)p.pair_ctas);
+        } else {
+            attr[1].val.clusterDim.x = (unsigned)p.splits;
+            attr[1].val.clusterDim.y = (unsigned)p.group;
+            cfg.gridDim = dim3((unsigned)p.splits, (unsigned)(p.Co / 128), (unsigned)p.passes);
+        }
         cfg.blockDim = dim3((unsigned)product_threads(p.own_digits != 0));
         cfg.dynamicSmemBytes = kSmem;
         return cudaLaunchKernelEx(&cfg, product, tm_w, tm_s, tm_x, tm_l2, tm_u, p);
