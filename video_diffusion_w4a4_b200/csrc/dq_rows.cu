@@ -19,7 +19,9 @@
 //                    one the digits, one issues scale copies and MMAs, eight write
 //                    the output.  When the tiles alone do not fill the GPU a cluster
 //                    splits the channels and sums its parts in order through
-//                    distributed shared memory.
+//                    distributed shared memory.  From three passes over the rows
+//                    on, CTA pairs (256 output channels, each CTA half of the digits'
+//                    columns) take one piece of work after another.
 //   k_rows_prepare   what it needs of the rows: digits and unit 2^(e-1), and U = xv
 //                    L1, which the product multiplies with L2 as BF16 K steps (hi +
 //                    lo) into columns of their own.
@@ -30,20 +32,22 @@
 // and whole ones, take a share of the channels of U each and exchange their sums
 // through distributed shared memory, so that L1 is read once a cluster.
 //
-// Bound: the weight's bytes (HBM) up to some 30 rows, then the digits' traffic from
-// L2 to the SMs, 4 bytes a value of X and tile of 128 output channels.  Measured on
-// B200, calls one after another on weights that are not in L2, against the time that
-// the bytes of weight, factors, X and Y need at the HBM's copy rate:
+// Bound: the weight's bytes (HBM) up to some 30 rows, then the digits: their MMAs and
+// their traffic from L2 to the SMs, 4 bytes a value of X and tile of 128 output
+// channels (2 with pairs).  Measured on B200, calls one after another on weights that
+// are not in L2, against the time that the bytes of weight, factors, X and Y need at
+// the HBM's copy rate:
 //   1 x 5120 -> 5120     9.4 us (2.4)      1 x 5120 -> 13824   13.7 us (6.3)
 //   4 x 13824 -> 5120   15.9 us (6.3)     21 x 5120 -> 13824   16.0 us (6.4)
-//   77 x 2048 -> 5120   12.0 us (1.3)    512 x 5120 -> 5120    62 us (4.0; 16 at the
+//   77 x 2048 -> 5120   12.2 us (1.3)    512 x 5120 -> 5120    57 us (4.0; 16 at the
 //   BF16 tensor rate)
 // The stream alone, the same copies without any MMAs, takes 3.3 us for 5120 -> 5120
 // and 7.1 us for 5120 -> 13824 (5.6 TB/s); a launch that waits for the one before it
 // starts some 2.7 us after that one's last CTA has left (1.7 us until its wait
 // returns, 1 us of setup), the first stage arrives 1.5 us later, and the output is
-// written 1.3 to 1.9 us after the last MMA.  At 512 rows the product's 55 us move 669 MB
-// from L2 to the SMs (12 TB/s, with the tensor pipe busy 46 % of the time).
+// written 1.3 to 1.9 us after the last MMA.  At 512 rows a pair's piece (5120 channels,
+// 30 rows) takes 7.1 us, of which 5.3 us are MMAs at the tensor pipe's full rate and
+// 1.8 us the accumulator's hand-over.
 //
 // MMAs: the four scale copies and four MMAs of a stage of 256 channels take 183
 // cycles with 8 columns, 336 with 168 and 512 with 256 (the tensor pipe's full rate),
