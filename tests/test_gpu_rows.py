@@ -402,6 +402,25 @@ def test_rows_with_more_work_than_fits_at_once(dq, Ci, Co, rank, rows):
         assert_within(run_rows(dq, dev, w, x, sc, fmt, gelu=fmt == 1, x_pad=16, y_pad=3), ref, tol, "Y")
 
 
+@pytest.mark.parametrize("fmt", [0, 2])
+def test_the_most_rows(dq, fmt):
+    """As many rows as a call takes, a few of them not finite, in the smallest layer."""
+    rows = 65535
+    w, dev = weight(dq, 256, 256, 16, seed=256, bias=True)
+    v, x, sc = rows_input(rows, 256, fmt, seed=1)
+    bad = [0, 31, 4096, rows - 1]
+    if fmt == 0:
+        x[bad, 77] = float("nan")
+    else:
+        sc[bad, 1] = float("inf")
+    y = run_rows(dq, dev, w, x, sc, fmt, x_pad=16)
+    ref, tol = rows_reference(w, v, False)
+    assert torch.isnan(y[bad].float()).all()
+    fine = torch.ones(rows, dtype=torch.bool)
+    fine[bad] = False
+    assert_within(y[fine], ref[fine], tol[fine], "Y")
+
+
 @pytest.mark.parametrize("rows", [4, 40])
 def test_rows_with_scales_that_are_not_finite(dq, rows):
     w, dev = weight(dq, 512, 768, 32, seed=512)
