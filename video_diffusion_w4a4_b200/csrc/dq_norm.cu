@@ -10,7 +10,9 @@
 // has at most 1024 channels, so that narrow rows need no block-wide step.
 // Eight neighbouring lanes hold 64 channels, so a group's maximum is three
 // shuffles.  Pointers, strides and widths that do not allow 16-byte pieces take
-// the same code with element accesses.
+// element accesses, for which a thread's channels are four pairs, a step of the
+// row's threads apart: a warp's access is 128 bytes in a row then, and a step of a
+// warp the 64 channels of a group.
 //
 // Measured on B200, residual added and stored, calls one after another:
 // 32760 x 5120 to BF16 200 us (6.7 TB/s, the rate of a plain copy), 1560 x 5120 to
@@ -19,6 +21,8 @@
 // Rows of 257 to 1024 pieces take two a thread in CTAs of at most 512 threads,
 // three or more to an SM: one piece a thread takes 16.9 us and 260 us, four CTAs'
 // worth of registers (32) 14.9 and 222 us, gamma loaded before the sum 14.1 and 224 us.
+// Element accesses: 1560 x 5119 to BF16 24 us, to E4M3 32 us per row and 35 us per group, 32760 x 1337 to
+// BF16 110 us (46, 38, 35 and 228 us with eight neighbouring channels a thread).
 #include <math.h>
 
 #include "dq_common.h"
@@ -56,54 +60,73 @@ __device__ __forceinline__ T row_reduce(T v, T* sh, Op op) {
     return v;
 }
 
-// Eight channels from c0 on (those below C); BF16 bits, the low half of a word first.
+// Channel of thread t's value j (even; j + 1 has the next) in piece i of a row that T threads share
 template <bool kWide>
-__device__ __forceinline__ void load8(const uint16_t* src, int c0, int C, uint32_t (&w)[4]) {
+__device__ __forceinline__ int channel(int t, int T, int i, int j) {
+    return kWide ? 8 * (t + i * T) + j : 2 * (t + (4 * i + j / 2) * T);
+}
+
+// Piece i of a row (zeros past its end); BF16 bits, the low half of a word first.
+template <bool kWide>
+__device__ __forceinline__ void load8(const uint16_t* src, int t, int T, int i, int C, uint32_t (&w)[4]) {
     if (kWide) {
-        const uint4 v = *reinterpret_cast<const uint4*>(src + c0);
+        const uint4 v = *reinterpret_cast<const uint4*>(src + channel<true>(t, T, i, 0));
         w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const uint32_t lo = c0 + 2 * i < C ? src[c0 + 2 * i] : 0, hi = c0 + 2 * i + 1 < C ? src[c0 + 2 * i + 1] : 0;
-            w[i] = lo | (hi << 16);
+        for (int k = 0; k < 4; k++) {
+            const int c = channel<false>(t, T, i, 2 * k);
+            const uint32_t lo = c < C ? src[c] : 0, hi = c + 1 < C ? src[c + 1] : 0;
+            w[k] = lo | (hi << 16);
         }
     }
 }
 
 template <bool kWide>
-__device__ __forceinline__ void store8(uint16_t* dst, int c0, int C, const float (&v)[8]) {
+__device__ __forceinline__ void store8(uint16_t* dst, int t, int T, int i, int C, const float (&v)[8]) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) w[i] = bf16x2_rn(v[2 * i], v[2 * i + 1]);
+    for (int k = 0; k < 4; k++) w[k] = bf16x2_rn(v[2 * k], v[2 * k + 1]);
     if (kWide) {
-        *reinterpret_cast<uint4*>(dst + c0) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(dst + channel<true>(t, T, i, 0)) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-            if (c0 + i < C) dst[c0 + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+        for (int k = 0; k < 4; k++) {
+            const int c = channel<false>(t, T, i, 2 * k);
+            if (c < C) dst[c] = (uint16_t)w[k];
+            if (c + 1 < C) dst[c + 1] = (uint16_t)(w[k] >> 16);
+        }
     }
 }
 
-// E4M3 codes of y / s, correctly rounded quotients; 0 where s is 0.
-template <bool kWide>
-__device__ __forceinline__ void store_codes8(uint8_t* dst, int c0, int C, const float (&y)[8], float s) {
-    uint32_t w[2] = {0, 0};
+// E4M3 codes of kPairs pairs y / s, two pairs a word, correctly rounded quotients; 0 where s is 0.
+template <int kPairs>
+__device__ __forceinline__ void codes(const float* y, float s, uint32_t* w) {
+#pragma unroll
+    for (int k = 0; k < (kPairs + 1) / 2; k++) w[k] = 0;
     if (s > 1e-30f && s < 1e30f) {
         const float rs = __frcp_rn(s);
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            w[i / 2] |= cvt_e4m3x2(div_pos(y[2 * i], s, rs), div_pos(y[2 * i + 1], s, rs)) << (16 * (i & 1));
+        for (int k = 0; k < kPairs; k++) w[k / 2] |= cvt_e4m3x2(div_pos(y[2 * k], s, rs), div_pos(y[2 * k + 1], s, rs)) << (16 * (k & 1));
     } else if (s != 0.f) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) w[i / 2] |= cvt_e4m3x2(__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s)) << (16 * (i & 1));
+        for (int k = 0; k < kPairs; k++) w[k / 2] |= cvt_e4m3x2(__fdiv_rn(y[2 * k], s), __fdiv_rn(y[2 * k + 1], s)) << (16 * (k & 1));
     }
+}
+
+// The codes of a piece, two pairs a word
+template <bool kWide>
+__device__ __forceinline__ void store_codes8(uint8_t* dst, int t, int T, int i, int C, const uint32_t (&w)[2]) {
     if (kWide) {
-        *reinterpret_cast<uint2*>(dst + c0) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(dst + channel<true>(t, T, i, 0)) = make_uint2(w[0], w[1]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-            if (c0 + i < C) dst[c0 + i] = (uint8_t)(w[i / 4] >> (8 * (i & 3)));
+        for (int k = 0; k < 4; k++) {
+            const int c = channel<false>(t, T, i, 2 * k);
+            const uint32_t two = w[k / 2] >> (16 * (k & 1));
+            if (c < C) dst[c] = (uint8_t)two;
+            if (c + 1 < C) dst[c + 1] = (uint8_t)(two >> 8);
+        }
     }
 }
 
@@ -123,19 +146,17 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kItems == 2 ? 512 : 1
     uint32_t xw[kItems][4], rw[kItems][4];
 #pragma unroll
     for (int i = 0; i < kItems; i++) {
-        const int c0 = 8 * (t + i * T);
-        if (c0 < p.C) {
-            load8<kWide>(x, c0, p.C, xw[i]);
-            if (p.residual) load8<kWide>(r, c0, p.C, rw[i]);
+        if (!kWide || channel<true>(t, T, i, 0) < p.C) {
+            load8<kWide>(x, t, T, i, p.C, xw[i]);
+            if (p.residual) load8<kWide>(r, t, T, i, p.C, rw[i]);
         }
     }
     float h[kItems][8], ss = 0.f;
 #pragma unroll
     for (int i = 0; i < kItems; i++) {
-        const int c0 = 8 * (t + i * T);
 #pragma unroll
         for (int j = 0; j < 8; j++) h[i][j] = 0.f;
-        if (c0 >= p.C) continue;
+        if (kWide && channel<true>(t, T, i, 0) >= p.C) continue;
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             h[i][2 * j] = bf16_lo(xw[i][j]), h[i][2 * j + 1] = bf16_hi(xw[i][j]);
@@ -143,7 +164,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kItems == 2 ? 512 : 1
         }
 #pragma unroll
         for (int j = 0; j < 8; j++) ss = fmaf(h[i][j], h[i][j], ss);
-        if (p.sum) store8<kWide>(p.sum + row * p.s_stride, c0, p.C, h[i]);
+        if (p.sum) store8<kWide>(p.sum + row * p.s_stride, t, T, i, p.C, h[i]);
     }
     ss = row_reduce<kWarp>(ss, sh[0], [](float a, float b) { return a + b; });
     const float v = ss / (float)p.C + p.eps;
@@ -166,38 +187,54 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kItems == 2 ? 512 : 1
     float am = 0.f;
 #pragma unroll
     for (int i = 0; i < kItems; i++) {
-        const int c0 = 8 * (t + i * T);
-        if (c0 < p.C) {
+        const bool in = !kWide || channel<true>(t, T, i, 0) < p.C;   // (pairs are looked at one by one)
+        if (in) {
             uint32_t gw[4];
-            if (p.gamma) load8<kWide>(p.gamma, c0, p.C, gw);
+            if (p.gamma) load8<kWide>(p.gamma, t, T, i, p.C, gw);
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 h[i][j] *= inv;
                 if (p.gamma) h[i][j] *= (j & 1) ? bf16_hi(gw[j / 2]) : bf16_lo(gw[j / 2]);
-            }
-            if (!kWide) {   // channels past the row's end take no part in a maximum (0 times infinity)
-#pragma unroll
-                for (int j = 0; j < 8; j++)
-                    if (c0 + j >= p.C) h[i][j] = 0.f;
+                // channels past the row's end take no part in a maximum (0 times infinity)
+                if (!kWide && channel<false>(t, T, i, j & ~1) + (j & 1) >= p.C) h[i][j] = 0.f;
             }
         }
         if (kOut == kOutBf16) {
-            if (c0 < p.C) store8<kWide>((uint16_t*)p.y + row * p.y_stride, c0, p.C, h[i]);
-        } else {
-            float a = fabsf(h[i][0]);
+            if (in) store8<kWide>((uint16_t*)p.y + row * p.y_stride, t, T, i, p.C, h[i]);
+        } else if (kOut == kOutRow) {
 #pragma unroll
-            for (int j = 1; j < 8; j++) a = max_nan(a, fabsf(h[i][j]));
-            if (kOut == kOutRow) {
-                am = max_nan(am, a);
-            } else {
+            for (int j = 0; j < 8; j++) am = max_nan(am, fabsf(h[i][j]));
+        } else {
+            uint32_t w[2] = {0, 0};
+            float* scales = p.scales + row * ((p.C + 63) / 64);
+            if (kWide) {
                 // 64 channels sit in eight neighbouring lanes
+                float a = fabsf(h[i][0]);
+#pragma unroll
+                for (int j = 1; j < 8; j++) a = max_nan(a, fabsf(h[i][j]));
 #pragma unroll
                 for (int o = 1; o < 8; o <<= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
                 const float s = a / 448.0f;
-                if (c0 < p.C) {
-                    store_codes8<kWide>((uint8_t*)p.y + row * p.y_stride, c0, p.C, h[i], s);
-                    if ((t & 7) == 0) p.scales[row * ((p.C + 63) / 64) + c0 / 64] = s;
+                if (in) {
+                    codes<4>(h[i], s, w);
+                    store_codes8<true>((uint8_t*)p.y + row * p.y_stride, t, T, i, p.C, w);
+                    if ((t & 7) == 0) scales[channel<true>(t, T, i, 0) / 64] = s;
                 }
+            } else {
+                // ... or in the pairs of a warp
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    float a = max_nan(fabsf(h[i][2 * k]), fabsf(h[i][2 * k + 1]));
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
+                    const float s = a / 448.0f;
+                    uint32_t two;
+                    codes<1>(&h[i][2 * k], s, &two);
+                    w[k / 2] |= (two & 0xFFFFu) << (16 * (k & 1));
+                    const int c = channel<false>(t, T, i, 2 * k);
+                    if ((t & 31) == 0 && c < p.C) scales[c / 64] = s;
+                }
+                store_codes8<false>((uint8_t*)p.y + row * p.y_stride, t, T, i, p.C, w);
             }
         }
     }
@@ -205,8 +242,10 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kItems == 2 ? 512 : 1
         const float s = row_reduce<kWarp>(am, sh[1], max_nan) / 448.0f;
 #pragma unroll
         for (int i = 0; i < kItems; i++) {
-            const int c0 = 8 * (t + i * T);
-            if (c0 < p.C) store_codes8<kWide>((uint8_t*)p.y + row * p.y_stride, c0, p.C, h[i], s);
+            if (kWide && channel<true>(t, T, i, 0) >= p.C) continue;
+            uint32_t w[2];
+            codes<4>(h[i], s, w);
+            store_codes8<kWide>((uint8_t*)p.y + row * p.y_stride, t, T, i, p.C, w);
         }
         if (t == 0) p.scales[row] = s;
     }
