@@ -598,7 +598,14 @@ int dq_rmsnorm_forward(const void* X, long long x_stride, const void* residual, 
  * xv is the row itself, not quantised further: BF16 values, or the values that
  * E4M3 codes and their scales stand for (x_format, DQ_ROWS_*).  act is the
  * identity or GELU (epilogue, DQ_EPILOGUE_*).  Sums are fp32, one rounding to
- * BF16 at the end.
+ * BF16 at the end.  The tensor cores take a row as fixed-point numbers of 24 bits
+ * below its largest magnitude M: E4M3 codes with one scale exactly, BF16 values of
+ * at least 2^(floor(log2 M) - 15) exactly, other values to 2^-23 M.  A row in which
+ * more than an eighth of the values other than zero are smaller than that bound is
+ * summed from its values as they are, in up to thirty times the time (with few rows
+ * the channels are judged in parts).  xv L1 is held in fp32 or as two BF16 numbers
+ * (2^-17 of its value).  Which of these a row takes depends on the shape, the row
+ * count and the device, so its bits may differ from those in a call of more rows.
  *   X        device, rows x Ci, BF16 (x_stride a multiple of 8) or E4M3 codes (a
  *            multiple of 16), 16-byte aligned
  *   x_scales device fp32, contiguous, as the format says (4-byte aligned); NULL

@@ -913,6 +913,7 @@ int dq_rows_forward(const void* X, int x_format, long long x_stride, const float
     p.y = (uint16_t*)Y;
     p.status = (int*)(ws + wl.off_status);
     p.e = (float*)(ws + wl.off_e);
+    p.span = (int*)(ws + wl.off_span);
     p.u = (uint16_t*)(ws + wl.off_u);
     p.digits = ws + wl.off_digits;
     p.budget_ns = kWaitBudgetNs;

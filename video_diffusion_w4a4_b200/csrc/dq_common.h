@@ -228,10 +228,13 @@ DQ_HD WsLayout ws_layout(const Geom& g, int Ci, int Co, int rank, int kgroup = 0
     return L;
 }
 
-// Workspace of dq_rows_forward: the status word, the rows' factors (fp32), U as BF16 hi + lo (rows x
-// slab) and the rows' FP4 digits (eight a value).
+// Parts of at most 8192 channels (eight for each of 1024 threads) that a row's preparation is cut into
+DQ_HD int rows_parts(int Ci) { return (Ci + 8191) / 8192; }
+
+// Workspace of dq_rows_forward: the status word, the rows' factors (fp32), how many binades their parts
+// span (int, rows x rows_parts), U as BF16 hi + lo (rows x slab) and the rows' FP4 digits (eight a value).
 struct RowsLayout {
-    size_t total, off_status, off_e, off_u, off_digits;
+    size_t total, off_status, off_e, off_span, off_u, off_digits;
 };
 
 DQ_HD RowsLayout rows_layout(int rows, int Ci, int rank) {
@@ -239,6 +242,7 @@ DQ_HD RowsLayout rows_layout(int rows, int Ci, int rank) {
     size_t off = 0;
     L.off_status = off;  off = align_up(off + 16, kAlign);
     L.off_e = off;       off = align_up(off + (size_t)rows * 4, kAlign);
+    L.off_span = off;    off = align_up(off + (size_t)rows * rows_parts(Ci) * 4, kAlign);
     L.off_u = off;       off = align_up(off + (size_t)rows * slab_width(rank) * 2, kAlign);
     L.off_digits = off;  off = align_up(off + (size_t)rows * Ci * 4, kAlign);
     L.total = off;

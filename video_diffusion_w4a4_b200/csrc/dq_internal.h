@@ -136,6 +136,7 @@ struct RowsParams {
     uint8_t* digits;            // rows x 8 x Ci/2: the rows' FP4 digits
     uint16_t* u;                // rows x slab BF16: X L1 as hi + lo
     float* e;                   // rows: what each row's sum of digits is multiplied by
+    int* span;                  // rows x parts: positive sum over a row's parts: it is summed without digits
     uint64_t budget_ns;
     // the cut of the product (rows_plan)
     int n_rows, n_pad, passes;  // rows of X per pass, their digits' columns

@@ -7,9 +7,16 @@
 // is written in the same format as kDigits = 8 FP4 digits a value,
 //   x = 2^(e-1) sum_p 8^-p d_p + r,   d_p in {-4, ..., 4},  |r| <= 2^(e-23),
 // with 2^e <= max |x| < 2^(e+1) over the row and d_p the nearest integer to what
-// the digits before it leave: 24 bits of the row's largest value, what an fp32 sum
-// over the row keeps of it.  Each digit is a column of the MMA (the B scales are 1)
-// and the epilogue sums a row's columns with their weights 8^-p in fp32.
+// the digits before it leave: 24 bits below the row's largest value.  Each digit is a
+// column of the MMA (the B scales are 1) and the epilogue sums a row's columns with
+// their weights 8^-p in fp32.
+//
+// Digits hold a BF16 value whole from 2^(e-15) on, and E4M3 codes with one scale always.
+// Smaller values lose bits, which an fp32 sum would keep where the weights of the larger
+// ones are zero.  So a row of which more than an eighth of the values other than zero lie
+// below 2^(e-15) is not taken from its digits: the epilogue forms its sums in fp32 from
+// the values themselves (wide_rows; span_sum has the rule).  Rows of normally distributed
+// values with outliers up to some 5000 times their deviation are on the digits' side.
 //
 // The low-rank factor is BF16 K steps of the same warp into columns of their own
 // (U = xv L1 as hi + lo, times L2).
@@ -165,6 +172,17 @@ __device__ __forceinline__ void mma_nvfp4(uint32_t d_tmem, uint64_t adesc, uint6
         : "memory");
 }
 
+// The two E2M1 codes of a byte -> FP16 pair (exact), the low nibble's in the low half
+__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t codes) {
+    uint32_t h2;
+    asm("{\n\t.reg .b8 t;\n\t"
+        "cvt.u8.u32 t, %1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
+        : "=r"(h2)
+        : "r"(codes));
+    return h2;
+}
+
 // Two E4M3 codes -> FP16 pair (exact), the low byte's in the low half
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
     uint32_t h2;
@@ -315,6 +333,37 @@ __device__ __forceinline__ void scaled_pairs(const float (&v)[8], Scale2 s, bool
     for (int i = 0; i < 4; i++) o[i] = finite ? f2_mul(f2_mul(f2_pack(v[2 * i], v[2 * i + 1]), a), b) : 0ull;
 }
 
+// A row's values v 2^-k count 7 where they are below 2^-14 (below 2^(e-15) of the row, where BF16 values lose
+// bits as digits), -1 where they are not and nothing where they are zero: positive for a row of which more than
+// an eighth is too small.  `v` and `raw` are the same eight values.
+template <int kFmt>
+__device__ __forceinline__ int span_sum(const Raw8<kFmt>& raw, const uint64_t (&v)[4], int k) {
+    if (kFmt == DQ_ROWS_E4M3) return 0;   // exact in eight digits
+    int sum = 0;
+    if (kFmt == DQ_ROWS_BF16) {
+        // by halves of a word: adding 2^15 less a bound sets a half's high bit from that bound on
+        const int te = k + 1 - 15 + 127;
+        const uint32_t small = (0x8000u - (te > 0 ? (uint32_t)te << 7 : 1u)) * 0x10001u;
+        uint32_t large = 0, any = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint32_t a = raw.w[i % (kFmt == DQ_ROWS_BF16 ? 4 : 2)] & 0x7FFF7FFFu;
+            large |= ((a + small) & 0x80008000u) >> i;
+            any |= ((a + 0x7FFF7FFFu) & 0x80008000u) >> i;
+        }
+        sum = 7 * __popc(any) - 8 * __popc(large);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            float a, b;
+            f2_unpack(v[i], a, b);
+            sum += fabsf(a) >= 0x1p-14f ? -1 : a != 0.f ? 7 : 0;
+            sum += fabsf(b) >= 0x1p-14f ? -1 : b != 0.f ? 7 : 0;
+        }
+    }
+    return sum;
+}
+
 // Channels 64 b + 16 t to + 15 of the rows m0 + g and m0 + g + 8 (the second unless kHalf) as BF16 pairs (zeros from
 // row nm on), and their scales where the format has one per 64 channels.
 template <int kFmt, bool kHalf>
@@ -348,9 +397,8 @@ __device__ __forceinline__ void load_rows_16(const RowsParams& p, int m0, int nm
 // (77 rows of 2048: 12 us for the call, 14.8 us with 1024 threads whatever the row; 512 threads whatever the row
 // cost 512 rows of 5120 7 us.)
 constexpr int kPrepThreads = 1024, kPrepCluster = 8;
-__host__ __device__ inline int prep_parts(int Ci) { return (Ci + 8 * kPrepThreads - 1) / (8 * kPrepThreads); }
 inline int prep_threads(int Ci) {
-    const int warps = (int)cdiv(Ci, 256 * prep_parts(Ci));
+    const int warps = (int)cdiv(Ci, 256 * rows_parts(Ci));
     return 32 * (warps < 8 ? 8 : warps);
 }
 
@@ -360,8 +408,11 @@ inline int prep_threads(int Ci) {
 template <int kFmt>
 __device__ __forceinline__ void digits_blocks(const RowsParams& p, int first, int step) {
     __shared__ float sh[2][kPrepThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, channels = 8 * (int)blockDim.x, parts = prep_parts(p.Ci), all = p.rows * parts;
+    __shared__ int span[2];
+    const int tid = threadIdx.x, lane = tid & 31, channels = 8 * (int)blockDim.x, parts = rows_parts(p.Ci), all = p.rows * parts;
     if (first >= all) return;
+    if (tid < 2) span[tid] = 0;   // (the loop's barriers are between this and the sums)
+    int last = -1;                // the piece before this one
     int m = parts == 1 ? first : first / parts, c = (first - m * parts) * channels + tid * 8;
     Raw8<kFmt> next = {};
     if (c < p.Ci) next = load_raw8<kFmt>(p, m, c);
@@ -382,19 +433,30 @@ __device__ __forceinline__ void digits_blocks(const RowsParams& p, int first, in
         if (lane == 0) sh[turn][tid >> 5] = am;
         __syncthreads();
         if (at >= all) griddep_launch();   // the CTA's loads have arrived
+        // the piece before this one: its span is summed, as every thread is past that
+        if (kFmt != DQ_ROWS_E4M3 && tid == 0 && last >= 0) p.span[last] = span[turn ^ 1], span[turn ^ 1] = 0;
+        last = row * parts + (here - tid * 8) / channels;
         am = sh[turn][0];
         for (int w = 1; w < (int)blockDim.x / 32; w++) am = max_nan(am, sh[turn][w]);
         const bool finite = finite_row(am);
         const int k = unit_exponent(am);
         if (here == 0) p.e[row] = row_factor<kFmt>(p, row, k, finite);
-        if (here >= p.Ci) continue;
         float v[8];
         uint64_t v2[4];
         values8<kFmt>(raw, v);
         scaled_pairs(v, inv_scale(k), finite, v2);
+        if (kFmt != DQ_ROWS_E4M3) {
+            const int s = __reduce_add_sync(0xffffffffu, finite ? span_sum<kFmt>(raw, v2, k) : 0);
+            if (lane == 0) atomicAdd(&span[turn], s);
+        }
+        if (here >= p.Ci) continue;
         uint8_t* dst = p.digits + (size_t)row * kDigits * (p.Ci / 2) + here / 2;
 #pragma unroll
         for (int q = 0; q < kDigits; q++) *reinterpret_cast<uint32_t*>(dst + (size_t)q * (p.Ci / 2)) = next_digits8(v2);
+    }
+    if (kFmt != DQ_ROWS_E4M3) {
+        __syncthreads();
+        if (tid == 0) p.span[last] = span[(all - 1 - first) / step & 1];
     }
 }
 
@@ -530,6 +592,7 @@ struct Ring {
 struct Bars {
     uint64_t full[kStages], empty[kStages], accf, acce, digits[kOwnTurns], u;
     float e[2][kPassRows];   // the rows' factors
+    alignas(16) int span[2][kPassRows];  // positive: the row's values take the place of its digits
     float amax[8];        // own digits: each warp's part of its row's largest magnitude
     uint32_t tmem;
     int abort_flag;
@@ -577,6 +640,7 @@ __device__ __forceinline__ void write_own_digits(const RowsParams& p, Bars& bars
     const int k = unit_exponent(am);
     if (m < p.rows && part == 0 && lane == 0) bars.e[0][m] = row_factor<kFmt>(p, m, k, finite);
     const Scale2 s = inv_scale(k);
+    int span = 0;
 #pragma unroll
     for (int i = 0; i < kOwnTurns; i++) {
         const int c = first + i * per * 256;
@@ -586,6 +650,7 @@ __device__ __forceinline__ void write_own_digits(const RowsParams& p, Bars& bars
                 uint64_t v2[4];
                 values8<kFmt>(raw[i], v);
                 scaled_pairs(v, s, finite, v2);
+                if (finite) span += span_sum<kFmt>(raw[i], v2, k);
                 // column 8 m + q of the 256-channel stage c / 256: row 8 m + q of 128 bytes, its 16-byte pieces
                 // permuted by the row's low bits (128-byte swizzle)
                 uint8_t* row = dst + (size_t)(c >> 8) * p.n_pad * 128 + m * 1024 + ((c >> 1) & 15);
@@ -599,6 +664,92 @@ __device__ __forceinline__ void write_own_digits(const RowsParams& p, Bars& bars
             if (lane == 0) mbar_arrive(&bars.digits[i]);
         }
     }
+    if (kFmt != DQ_ROWS_E4M3) {   // read behind the epilogue warps' next barrier
+        span = __reduce_add_sync(0xffffffffu, span);
+        if (m < p.rows && lane == 0) atomicAdd(&bars.span[0][m], span);
+    }
+}
+
+// The sums sum_c (x_c 2^-k) (q s_b)[o + lane][c] over the channels 64 b0 to 64 b1 - 1 for the rows m to m + 3 (those
+// below m + nm) and a warp's 32 output channels, from the values as they are: BF16 operands (weights q s_b, BF16 values and
+// E4M3 codes are exact in BF16), fp32 sums, and the scale of a row's 64 channels on their sum.  `e` holds the rows' units
+// 2^k.  Bound by the latency of its loads: 1 x 5120 -> 5120 takes 28 us with it, 512 x 5120 -> 5120 130 us where one
+// row needs it and 1.7 ms where all do (the digits alone 8.7 and 59 us).  The next block's loads ahead of this one's
+// products take a fifth off that, and cost the rows that do not need it 0.6 us in registers.
+__device__ __forceinline__ float4 wide_rows(const uint8_t* codes, const uint8_t* scales, const void* x, long long x_stride,
+                                         const float* x_scales, int Ci, int o, int m, int nm, int b0, int b1, const float* e) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float acc[2][4] = {}, inv[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) inv[i] = 2 * t + i < imin(nm, 4) ? __frcp_rn(e[2 * t + i]) : 0.f;
+    const float inv_g = g < imin(nm, 4) ? __frcp_rn(e[g]) : 0.f;
+    const __nv_bfloat162 unit = __float2bfloat162_rn(inv_g);
+#pragma unroll 1
+    for (int b = b0; b < b1; b++) {
+        uint32_t xa[8] = {};
+        float sc[2] = {1.f, 1.f};
+        if (g < imin(nm, 4)) {
+            const long long off = (long long)(m + g) * x_stride + b * 64 + t * 16;
+            if (!x_scales) {
+                const uint4* src = reinterpret_cast<const uint4*>((const uint16_t*)x + off);
+                const uint4 u = src[0], v = src[1];
+                const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const __nv_bfloat162 s = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), unit);
+                    xa[i] = *reinterpret_cast<const uint32_t*>(&s);
+                }
+            } else {
+                const uint4 u = *reinterpret_cast<const uint4*>((const uint8_t*)x + off);
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int i = 0; i < 8; i++) xa[i] = e4m3x2_to_bf16x2(w[i / 2] >> (16 * (i & 1)));
+            }
+        }
+        if (x_scales) {
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+                sc[i] = 2 * t + i < imin(nm, 4) ? x_scales[(long long)(m + 2 * t + i) * (Ci / 64) + b] * inv[i] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            uint32_t w[2][8];   // the channels 16 t to + 15 of the block, one group scale: any order of channels that both share
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int row = o + 16 * j + 8 * h + g;
+                const uint2 q = *reinterpret_cast<const uint2*>(codes + (long long)row * (Ci / 2) + b * 32 + t * 8);
+                const float s = e4m3_to_f32(scales[sfb_offset(row, 4 * b + t, Ci)]);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    float lo, hi;
+                    f16x2_values(e2m1x2_to_f16x2((i < 4 ? q.x : q.y) >> (8 * (i & 3))), lo, hi);
+                    w[h][i] = bf16x2_rn(lo * s, hi * s);
+                }
+            }
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) mma_16816(d, w[0][i], w[1][i], w[0][i + 1], w[1][i + 1], xa[i], xa[i + 1]);
+#pragma unroll
+            for (int i = 0; i < 4; i++) acc[j][i] = fmaf(d[i], sc[i & 1], acc[j][i]);
+        }
+    }
+    // lane (g, t) has the rows 2 t and 2 t + 1 of the channels g, g + 8, g + 16, g + 24: each lane takes its channel's
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int from = (lane & 7) * 4 + i / 2;
+        const float a = __shfl_sync(0xffffffffu, acc[0][i & 1], from), b = __shfl_sync(0xffffffffu, acc[0][2 + (i & 1)], from);
+        const float c = __shfl_sync(0xffffffffu, acc[1][i & 1], from), d = __shfl_sync(0xffffffffu, acc[1][2 + (i & 1)], from);
+        v[i] = lane < 8 ? a : lane < 16 ? b : lane < 24 ? c : d;
+    }
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// As a call of its own it leaves the one-launch form its registers (5120 -> 5120 8.7 us, 8.8 us inline); in the others
+// the call costs more than it spares (21 x 5120 -> 13824 16.5 us, 16.3 us inline; 512 x 5120 -> 5120 62.6 and 60.3 us).
+__device__ __noinline__ float4 wide_rows_call(const uint8_t* codes, const uint8_t* scales, const void* x, long long x_stride,
+                                              const float* x_scales, int Ci, int o, int m, int nm, int b0, int b1, const float* e) {
+    return wide_rows(codes, scales, x, x_stride, x_scales, Ci, o, m, nm, b0, b1, e);
 }
 
 // Low-rank term beside the product (at most kOwnRows rows): this CTA's share of the channels of U, cut further among
@@ -682,8 +833,10 @@ __device__ __forceinline__ void lowrank_term(const RowsParams& p, Bars& bars, fl
 // (two tiles of output channels, each CTA with half of the digits' columns in its shared memory).
 enum { kPrepared = 0, kOwnDigits = 1, kPairs = 2 };
 
+// Registers a thread: 80 for prepared rows and 96 (the one-launch form's 640 threads) otherwise, as wide_rows would take
+// up to 168, with which k_rows_prepare's CTAs do not fit beside this kernel's (the same times within 1 %).
 template <int kFmt, int kForm>
-__global__ void __launch_bounds__(product_threads(kForm == kOwnDigits), 1)
+__global__ void __launch_bounds__(product_threads(kForm != kPrepared), kForm == kPrepared ? 2 : 1)
     k_rows_product(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_s,
                    const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_l2,
                    const __grid_constant__ CUtensorMap tm_u, RowsParams p) {
@@ -733,6 +886,7 @@ __global__ void __launch_bounds__(product_threads(kForm == kOwnDigits), 1)
             tmem_relinquish();
         }
     }
+    if (tid >= 128 && tid < 128 + 2 * kPassRows) (&bars.span[0][0])[tid - 128] = 0;   // also of rows that there are not
     if (warp == 0 && lane == 0) {
         prefetch_tmap(&tm_w);
         prefetch_tmap(&tm_s);
@@ -917,6 +1071,34 @@ __global__ void __launch_bounds__(product_threads(kForm == kOwnDigits), 1)
     bool done = true, ok = true;
     float S_W = 0.f;
     const bool epi = warp >= 4 && warp < 12;
+    // Row m0 + et's factor and span, from k_rows_prepare
+    auto load_factors = [&](int buf) {
+        const int parts = rows_parts(p.Ci);
+        int span = 0;
+        const float e = p.e[m0 + et];
+        if (p.x_format != DQ_ROWS_E4M3)
+            for (int i = 0; i < parts; i++) span += p.span[(m0 + et) * parts + i];
+        bars.e[buf][et] = e;
+        bars.span[buf][et] = span;
+    };
+    uint32_t used = 0;   // pieces so far
+    // Rows that are not taken from their digits: their sums, ready before the accumulator is
+    float4 wide[kPassRows / 8];
+    bool any_wide = false;
+    auto spans = [&](int b) { return *reinterpret_cast<const int4*>(&bars.span[used & 1][4 * b]); };
+    auto form_wide = [&] {
+        if (kFmt == DQ_ROWS_E4M3) return;
+        any_wide = false;
+#pragma unroll 1
+        for (int b = group; 4 * b < nm; b += 2) {
+            const int4 s = spans(b);
+            if (s.x > 0 || s.y > 0 || s.z > 0 || s.w > 0) {
+                any_wide = true;
+                wide[b >> 1] = (own ? wide_rows_call : wide_rows)(p.packed_w + p.off_codes, p.packed_w + p.off_scales, p.x, p.x_stride, p.x_scales, p.Ci,
+                                         o0 + quad * 32, m0 + 4 * b, nm - 4 * b, a0 * 4, (a0 + nA) * 4, &bars.e[used & 1][4 * b]);
+            }
+        }
+    };
     uint32_t flags = 0;
     float bias = 0.f;
     if (own && warp < 4) cluster_wait();
@@ -939,11 +1121,12 @@ __global__ void __launch_bounds__(product_threads(kForm == kOwnDigits), 1)
             cluster_wait();
         } else {
             griddep_wait();   // the rows' factors come from k_rows_prepare
-            if (!pairs && et < nm) bars.e[0][et] = p.e[m0 + et];
+            if (!pairs && et < nm) load_factors(0);
         }
         ok = header_ok(p);
         if (!pairs) {
             bar_sync(1, kEpiThreads);
+            form_wide();
             if (own) bar_sync(5, 512);   // the low-rank term
             if (lane == 0) done = mbar_wait(&bars.accf, 0, abort_flag, p.status, p.budget_ns);
             done = __shfl_sync(0xffffffffu, done, 0);
@@ -952,7 +1135,6 @@ __global__ void __launch_bounds__(product_threads(kForm == kOwnDigits), 1)
     }
     if (own && tid == 96 && blockIdx.x + blockIdx.y + blockIdx.z == 0) *p.status = header_ok(p) ? 0 : kStatusBadWeight;
     float bv = (flags & kPackedHasBias) ? bias : 0.f;
-    uint32_t used = 0;   // pieces so far
     // This CTA's part of the rows 4 b to 4 b + 3 for the thread's output channel: the digits' columns with
     // weights 8^-p, times S_W and the row's factor, and U L2 where this CTA has it
     auto parts_of = [&](int b, float (&v)[4]) {
@@ -966,8 +1148,17 @@ __global__ void __launch_bounds__(product_threads(kForm == kOwnDigits), 1)
             v[i] = __uint_as_float(acc[kDigits * i + kDigits - 1]);
 #pragma unroll
             for (int q = kDigits - 2; q >= 0; q--) v[i] = fmaf(v[i], 0.125f, __uint_as_float(acc[kDigits * i + q]));
-            v[i] = fmaf(v[i] * S_W, bars.e[used & 1][imin(4 * b + i, nm - 1)], !own && split == 0 ? __uint_as_float(low[i]) : 0.f);
         }
+        if (kFmt != DQ_ROWS_E4M3 && (own || any_wide)) {
+            const int4 s = spans(b);
+            if (s.x > 0) v[0] = wide[b >> 1].x;
+            if (s.y > 0) v[1] = wide[b >> 1].y;
+            if (s.z > 0) v[2] = wide[b >> 1].z;
+            if (s.w > 0) v[3] = wide[b >> 1].w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            v[i] = fmaf(v[i] * S_W, bars.e[used & 1][imin(4 * b + i, nm - 1)], !own && split == 0 ? __uint_as_float(low[i]) : 0.f);
     };
     // Y of the thread's output channel for the i-th of the rows split, split + splits, ... that this CTA finishes, and
     // for the next where there is one
@@ -986,8 +1177,9 @@ __global__ void __launch_bounds__(product_threads(kForm == kOwnDigits), 1)
         for (int item = item0; item < items && epi; item += step, used++) {
             o0 = tile_of(item), m0 = rows_of(item), mine = nm = imin(p.n_rows, p.rows - m0);
             if (used && (flags & kPackedHasBias)) bv = *(const float*)(p.packed_w + p.off_bias + 4ll * (o0 + row));
-            if (et < nm) bars.e[used & 1][et] = p.e[m0 + et];
+            if (et < nm) load_factors(used & 1);
             bar_sync(1, kEpiThreads);
+            form_wide();
             // (a warp whose wait has run out goes on without writing, as the others still meet it at the barrier)
             bool full = true;
             if (lane == 0) full = mbar_wait(&bars.accf, used & 1, abort_flag, p.status, p.budget_ns);
@@ -1153,7 +1345,7 @@ cudaError_t prepare_plan(RowsParams& p) {
     // the others take piece after piece.  5120 -> 5120: 256 rows 42.1 us either way, 512 rows 71 us against 62 us;
     // 256 rows 5120 -> 13824: 76.5 us against 79 us.
     const long long fit = (long long)sms * (1024 / prep_threads(p.Ci)), groups = cdiv(p.rows, 16) * cdiv(p.rank, 32);
-    long long pieces = (long long)p.rows * prep_parts(p.Ci);
+    long long pieces = (long long)p.rows * rows_parts(p.Ci);
     p.prep_cluster = kPrepCluster;
     if (groups * kPrepCluster + pieces > 4 * fit) {
         while (p.prep_cluster > 1 && groups * p.prep_cluster > fit / 2) p.prep_cluster /= 2;
