@@ -619,7 +619,8 @@ int dq_rmsnorm_forward(const void* X, long long x_stride, const void* residual, 
  * memory; a larger row count's workspace serves smaller ones too.  Calls that
  * may overlap need workspaces of their own (two captured graphs too).  Every
  * call sets the status word (dq_read_device_status) anew: a packed weight that
- * does not match is DQ_ERR_BAD_PACKED_WEIGHT, and Y is then not written.  A row
+ * does not match is DQ_ERR_BAD_PACKED_WEIGHT; nothing but its header is then read
+ * and Y is not written.  A row
  * of X with a NaN or an infinity gives a row of NaN.  Only the Co values of each
  * row of Y are written; Y must not overlap X.
  */

@@ -134,3 +134,30 @@ def test_values_at_the_ends_of_the_range(dq):
         torch.cuda.synchronize()
         ref, tol = reference(w, x[:rows].double(), 0)
         assert_within(y, ref, tol, "Y")
+
+
+@pytest.mark.parametrize("Ci,Co,rank,rows", [(512, 768, 32, 1), (512, 768, 32, 8), (512, 768, 32, 20), (768, 5120, 48, 155),
+                                             (8448, 256, 16, 2)])
+def test_of_a_weight_that_does_not_match_only_the_header_is_read(dq, Ci, Co, rank, rows):
+    """A blob of 256 bytes, as a smaller layer's may end behind what this call's sizes point to; wide rows among the
+    others.  A right weight at the same address is taken by the next call."""
+    w, dev = blind_weight(dq, Ci, Co, rank, [Ci // 2 + 5])
+    v, x, _ = wide_rows(rows, Ci, 0, 20, [Ci // 2 + 5], seed=rows)
+    other, _ = blind_weight(dq, 256, 256, 16, [1])
+    ws = torch.full((dq.dq_rows_workspace_bytes(rows, Ci, Co, rank),), 0xFF, dtype=torch.uint8, device="cuda")
+    for head in (torch.from_numpy(other.packed[:256].copy()).cuda(), torch.zeros(256, dtype=torch.uint8, device="cuda")):
+        y = torch.full((rows, Co), -7.0, dtype=torch.bfloat16, device="cuda")
+        dq.dq_rows_forward(x.cuda(), rows, Ci, Co, rank, head, *dev[1:], y, ws, ws.numel())
+        torch.cuda.synchronize()
+        assert dq.dq_read_device_status(ws) == dq.DQ_ERR_BAD_PACKED_WEIGHT
+        assert (y == -7).all()
+    blob = torch.zeros_like(dev[0])
+    xd, y = x.cuda(), torch.full((rows, Co), -7.0, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    dq.dq_rows_forward(xd, rows, Ci, Co, rank, blob, *dev[1:], y, ws, ws.numel())
+    blob.copy_(dev[0])
+    dq.dq_rows_forward(xd, rows, Ci, Co, rank, blob, *dev[1:], y, ws, ws.numel())
+    torch.cuda.synchronize()
+    assert dq.dq_read_device_status(ws) == 0
+    ref, tol = reference(w, v, 0)
+    assert_within(y, ref, tol, "Y")

@@ -199,10 +199,26 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-__device__ __forceinline__ bool header_ok(const RowsParams& p) {
-    const PackedHeader* h = reinterpret_cast<const PackedHeader*>(p.packed_w);
-    return h->magic == DQ_PACK_MAGIC && h->version == DQ_PACK_FORMAT_VERSION && h->Ci == p.Ci && h->Co == p.Co &&
-           h->rank == p.rank && h->slab == p.slab;
+// The packed weight's header up to its flags: magic, version, Co, Ci; rank, slab, S_W, flags.
+struct Header {
+    uint4 a, b;
+};
+__device__ __forceinline__ Header load_header(const RowsParams& p) {
+    const uint4* h = reinterpret_cast<const uint4*>(p.packed_w);
+    return Header{h[0], h[1]};
+}
+
+// ... ahead of the launches before this one, so that no L1 keeps it
+__device__ __forceinline__ Header early_header(const RowsParams& p) {
+    const uint4* h = reinterpret_cast<const uint4*>(p.packed_w);
+    return Header{__ldcv(h), __ldcv(h + 1)};
+}
+
+// Nothing of a packed weight but its header may be read before this holds: its sections lie where this call's sizes
+// say, and a weight of other sizes may end before them.  (The wait for it before the stream: 0.4 us of a call.)
+__device__ __forceinline__ bool header_ok(const Header& h, const RowsParams& p) {
+    return h.a.x == DQ_PACK_MAGIC && h.a.y == DQ_PACK_FORMAT_VERSION && (int)h.a.z == p.Co && (int)h.a.w == p.Ci &&
+           (int)h.b.x == p.rank && (int)h.b.y == p.slab;
 }
 
 __device__ __forceinline__ void f16x2_values(uint32_t h2, float& lo, float& hi) {
@@ -567,7 +583,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_rows_prepare(RowsParams p) {
     __shared__ float wpart[16][16][32], part[16][32];
     // the low-rank clusters first: they take longest
     const int b = (int)blockIdx.x, low = (p.rows + 15) / 16 * ((p.rank + 31) / 32) * p.prep_cluster;
-    if (b == 0 && threadIdx.x == 0) *p.status = header_ok(p) ? 0 : kStatusBadWeight;
+    if (b == 0 && threadIdx.x == 0) *p.status = header_ok(load_header(p), p) ? 0 : kStatusBadWeight;
     if (b < low)
         lowrank_cluster<kFmt>(p, b / p.prep_cluster, wpart, part);
     else
@@ -593,6 +609,10 @@ struct Bars {
     uint64_t full[kStages], empty[kStages], accf, acce, digits[kOwnTurns], u;
     float e[2][kPassRows];   // the rows' factors
     alignas(16) int span[2][kPassRows];  // positive: the row's values take the place of its digits
+    alignas(16) float bias[128];
+    float S_W;               // of the weight's header, with its flags, and whether it is this call's
+    uint32_t flags;
+    int fits;
     float amax[8];        // own digits: each warp's part of its row's largest magnitude
     uint32_t tmem;
     int abort_flag;
@@ -864,6 +884,10 @@ __global__ void __launch_bounds__(product_threads(kForm != kPrepared), kForm == 
     float* slow = su + 8 * p.rank;
     const uint32_t n16 = (uint32_t)(p.n_rows + 15) & ~15u;
     volatile int* abort_flag = &bars.abort_flag;
+    // The header, on its way beside the setup: it lets the weight's loads start.  What is written to Y and reported goes
+    // by another look at it behind the launches before this one, which may only now be writing it.
+    Header early = {};
+    if (warp == 0) early = early_header(p);
 
     if (tid == 0) {
         for (int s = 0; s < S; s++) {
@@ -925,13 +949,16 @@ __global__ void __launch_bounds__(product_threads(kForm != kPrepared), kForm == 
             Ring r;
             int n = 0;   // stages so far
             bool ok = true;
+            const bool good = header_ok(early, p) || header_ok(load_header(p), p);   // else the stages stay as they are, and so does Y
             for (int item = item0; item < items && ok; item += step) {
                 const int o = tile_of(item), half = (o >> 7) & 1, blk0 = (o >> 8) * (p.Ci / 64) + a0 * 4;
                 for (int g = 0; g < total; g++, n++, r.next(S)) {
                     uint64_t* full = &bars.full[r.slot];
                     if (n >= S && !(ok = mbar_wait(&bars.empty[r.slot], r.phase ^ 1, abort_flag, p.status, p.budget_ns))) break;
                     uint8_t* dst = sm + (size_t)r.slot * stage;
-                    if (pairs) {
+                    if (!good) {
+                        if (lead) mbar_arrive(full);
+                    } else if (pairs) {
                         if (lead) mbar_arrive_expect_tx(full, 2 * (g < nA ? kCodeBytes + kScaleBytes : kCodeBytes));
                         const uint32_t at = mapa_shared(smem_u32(full), 0);
                         if (g < nA) {
@@ -1064,10 +1091,25 @@ __global__ void __launch_bounds__(product_threads(kForm != kPrepared), kForm == 
         __syncwarp();
     }
 
+    if (warp == 3) {
+        // ------------------------------------------------ the header, S_W and the bias (the first piece's), for the epilogue
+        const Header h = load_header(p);
+        const bool fits = header_ok(h, p);
+        float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (fits && (h.b.w & kPackedHasBias)) b = *reinterpret_cast<const float4*>(p.packed_w + p.off_bias + 4ll * (o0 + 4 * lane));
+        *reinterpret_cast<float4*>(&bars.bias[4 * lane]) = b;
+        if (lane == 0) {
+            bars.S_W = __uint_as_float(h.b.z);
+            bars.flags = h.b.w;
+            bars.fits = fits;
+        }
+        __syncwarp();
+        bar_arrive(6, 32 + kEpiThreads);
+    }
+
     // ---------------------------------------------------- epilogue warps
     const int quad = warp & 3, group = (warp - 4) >> 2, row = quad * 32 + lane, et = tid - 128;
     const uint32_t trow = (uint32_t)(quad * 32) << 16;
-    const PackedHeader* hdr = reinterpret_cast<const PackedHeader*>(p.packed_w);
     bool done = true, ok = true;
     float S_W = 0.f;
     const bool epi = warp >= 4 && warp < 12;
@@ -1087,7 +1129,7 @@ __global__ void __launch_bounds__(product_threads(kForm != kPrepared), kForm == 
     bool any_wide = false;
     auto spans = [&](int b) { return *reinterpret_cast<const int4*>(&bars.span[used & 1][4 * b]); };
     auto form_wide = [&] {
-        if (kFmt == DQ_ROWS_E4M3) return;
+        if (kFmt == DQ_ROWS_E4M3 || !ok) return;
         any_wide = false;
 #pragma unroll 1
         for (int b = group; 4 * b < nm; b += 2) {
@@ -1099,16 +1141,12 @@ __global__ void __launch_bounds__(product_threads(kForm != kPrepared), kForm == 
             }
         }
     };
-    uint32_t flags = 0;
-    float bias = 0.f;
+    float bv = 0.f;
     if (own && warp < 4) cluster_wait();
     if (own && warp >= 12) lowrank_term<kFmt>(p, bars, up, su, slow, o0, crank, csize, split, splits);
     if (epi) {
         Raw8<kFmt> raw[kOwnTurns];
         if (own) load_own_rows<kFmt>(p, a0 * 256, nA * 256, raw);
-        flags = hdr->flags;
-        bias = *(const float*)(p.packed_w + p.off_bias + 4ll * (o0 + row));
-        S_W = hdr->S_W;
         if (own) bar_arrive(3, 32 + 512);   // the weight may follow
         if (!pairs && warp < 8) {
             ones(t_one + trow);
@@ -1123,7 +1161,10 @@ __global__ void __launch_bounds__(product_threads(kForm != kPrepared), kForm == 
             griddep_wait();   // the rows' factors come from k_rows_prepare
             if (!pairs && et < nm) load_factors(0);
         }
-        ok = header_ok(p);
+        bar_sync(6, 32 + kEpiThreads);
+        ok = bars.fits;
+        S_W = bars.S_W;
+        bv = bars.bias[row];
         if (!pairs) {
             bar_sync(1, kEpiThreads);
             form_wide();
@@ -1133,8 +1174,7 @@ __global__ void __launch_bounds__(product_threads(kForm != kPrepared), kForm == 
             tc_fence_after();
         }
     }
-    if (own && tid == 96 && blockIdx.x + blockIdx.y + blockIdx.z == 0) *p.status = header_ok(p) ? 0 : kStatusBadWeight;
-    float bv = (flags & kPackedHasBias) ? bias : 0.f;
+    if (own && tid == 96 && blockIdx.x + blockIdx.y + blockIdx.z == 0) *p.status = header_ok(load_header(p), p) ? 0 : kStatusBadWeight;
     // This CTA's part of the rows 4 b to 4 b + 3 for the thread's output channel: the digits' columns with
     // weights 8^-p, times S_W and the row's factor, and U L2 where this CTA has it
     auto parts_of = [&](int b, float (&v)[4]) {
@@ -1176,7 +1216,7 @@ __global__ void __launch_bounds__(product_threads(kForm != kPrepared), kForm == 
     if (pairs) {
         for (int item = item0; item < items && epi; item += step, used++) {
             o0 = tile_of(item), m0 = rows_of(item), mine = nm = imin(p.n_rows, p.rows - m0);
-            if (used && (flags & kPackedHasBias)) bv = *(const float*)(p.packed_w + p.off_bias + 4ll * (o0 + row));
+            if (used && ok && (bars.flags & kPackedHasBias)) bv = *(const float*)(p.packed_w + p.off_bias + 4ll * (o0 + row));
             if (et < nm) load_factors(used & 1);
             bar_sync(1, kEpiThreads);
             form_wide();
