@@ -649,6 +649,17 @@ int dq_read_device_status(const void* workspace, void* stream, int* status, int 
 int dq_selftest_bounded_wait(int budget_us, void* stream, int* status);
 
 /*
+ * The same for the exchange between the CTAs of a dq_rows_forward call of one
+ * launch: a call on contiguous BF16 rows in which that exchange waits for one
+ * arrival too many, with a wait budget of budget_us microseconds (at least 1000)
+ * for every wait.  The status word must come back as DQ_ERR_DEVICE_TIMEOUT and Y
+ * as it was.  DQ_ERR_UNSUPPORTED_SHAPE where the call takes two launches.
+ */
+int dq_selftest_rows_wait(int budget_us, const void* X, int rows, int Ci, int Co, int rank, const void* packed_W,
+                          const void* L1_mma, const void* L2_slab, void* Y, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/*
  * GELU self test: out[i] = the feed-forward epilogue's GELU of in[i] (DQ_EPILOGUE_GELU's
  * fp32 evaluation, two values at a time as the epilogue takes them), for n device fp32
  * values; asynchronous.

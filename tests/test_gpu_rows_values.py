@@ -161,3 +161,24 @@ def test_of_a_weight_that_does_not_match_only_the_header_is_read(dq, Ci, Co, ran
     assert dq.dq_read_device_status(ws) == 0
     ref, tol = reference(w, v, 0)
     assert_within(y, ref, tol, "Y")
+
+
+@pytest.mark.parametrize("Ci,Co,rank,rows", [(512, 768, 32, 1), (5120, 768, 80, 4), (1280, 2560, 32, 8)])
+def test_a_wait_that_runs_out_leaves_y_and_is_reported(dq, Ci, Co, rank, rows):
+    """The exchange of the low-rank sums waits for an arrival that never comes: the wait ends by its budget, the status
+    word says so whatever it was before, and Y stays as it was.  The next call is as ever."""
+    w, dev = blind_weight(dq, Ci, Co, rank, [5])
+    v, x, _ = wide_rows(rows, Ci, 0, 0, [5], seed=rows)
+    xd, y = x.cuda(), torch.full((rows, Co), -7.0, dtype=torch.bfloat16, device="cuda")
+    need = dq.dq_rows_workspace_bytes(rows, Ci, Co, rank)
+    for before in (0x00, 0xFF):
+        ws = torch.full((need,), before, dtype=torch.uint8, device="cuda")
+        dq.dq_selftest_rows_wait(50000, xd, rows, Ci, Co, rank, *dev, y, ws, need)
+        torch.cuda.synchronize()
+        assert dq.dq_read_device_status(ws) == dq.DQ_ERR_DEVICE_TIMEOUT
+        assert (y == -7).all()
+    dq.dq_rows_forward(xd, rows, Ci, Co, rank, *dev, y, ws, need)
+    torch.cuda.synchronize()
+    assert dq.dq_read_device_status(ws) == 0
+    ref, tol = reference(w, v, 0)
+    assert_within(y, ref, tol, "Y")

@@ -80,3 +80,9 @@ def test_reference_decodes_the_packed_weight():
     d = w.packed[lay.off_dqw:lay.off_dqw + 256 * 512 * 2].view(np.uint16).astype(np.uint32) << 16
     s_w = float(w.packed[24:28].view(np.float32)[0])
     assert np.array_equal(d.view(np.float32).astype(np.float64).reshape(256, 512) * s_w, w.values)
+
+
+def test_rows_wait_selftest_refusals():
+    call = lambda us=50000, m=4: dq._lib.dq_selftest_rows_wait(us, P, m, 512, 256, 32, P, P, P, P, P, 16, None)  # noqa: E731
+    assert call(us=999) == dq.DQ_ERR_INVALID_ARG and call(m=0) == dq.DQ_ERR_INVALID_ARG
+    assert call() == dq.DQ_ERR_WORKSPACE_TOO_SMALL

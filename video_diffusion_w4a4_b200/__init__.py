@@ -110,6 +110,7 @@ _SIGS = {
     "dq_rows_workspace_bytes": ([_I] * 4 + [ctypes.POINTER(_SZ)], _I),
     "dq_rows_forward": ([_P, _I, _LL, _P] + [_I] * 4 + [_P] * 3 + [_I, _P, _LL, _P, _SZ, _P], _I),
     "dq_selftest_bounded_wait": ([_I, _P, ctypes.POINTER(_I)], _I),
+    "dq_selftest_rows_wait": ([_I, _P] + [_I] * 4 + [_P] * 5 + [_SZ, _P], _I),
     "dq_selftest_convert": ([_P, _LL, _P, _P, _P, _P], _I),
     "dq_selftest_gelu": ([_P, _LL, _P, _P], _I),
     "dq_selftest_divide": ([_LL, ctypes.c_uint64, ctypes.POINTER(ctypes.c_ulonglong), _P, _P], _I),
@@ -501,6 +502,13 @@ def dq_selftest_bounded_wait(budget_us: int, stream=None) -> int:
 def dq_selftest_convert(inp, n, e2m1, e4m3, e4m3_value, stream=None) -> None:
     _check("dq_selftest_convert", _lib.dq_selftest_convert(_ptr(inp), n, _ptr(e2m1), _ptr(e4m3), _ptr(e4m3_value),
                                                            _stream(stream)))
+
+
+def dq_selftest_rows_wait(budget_us, X, rows, Ci, Co, rank, packed_W, L1_mma, L2_slab, Y, workspace, workspace_bytes,
+                          stream=None) -> None:
+    x, w, l1, l2, y, ws = _device_ptrs("dq_selftest_rows_wait", X, packed_W, L1_mma, L2_slab, Y, workspace)
+    _check("dq_selftest_rows_wait", _lib.dq_selftest_rows_wait(budget_us, x, rows, Ci, Co, rank, w, l1, l2, y, ws,
+                                                               workspace_bytes, _stream(stream)))
 
 
 def dq_selftest_gelu(inp, n, out, stream=None) -> None:

@@ -869,9 +869,10 @@ int dq_rows_workspace_bytes(int rows, int Ci, int Co, int rank, size_t* bytes) {
     return DQ_OK;
 }
 
-int dq_rows_forward(const void* X, int x_format, long long x_stride, const float* x_scales, int rows, int Ci, int Co,
-                    int rank, const void* packed_W, const void* L1_mma, const void* L2_slab, int epilogue, void* Y,
-                    long long y_stride, void* workspace, size_t workspace_bytes, void* stream) {
+static int rows_forward(const void* X, int x_format, long long x_stride, const float* x_scales, int rows, int Ci, int Co,
+                        int rank, const void* packed_W, const void* L1_mma, const void* L2_slab, int epilogue, void* Y,
+                        long long y_stride, void* workspace, size_t workspace_bytes, void* stream, uint64_t budget_ns,
+                        int u_missing) {
     int rc = check_rows_shape(rows, Ci, Co, rank);
     if (rc) return rc;
     if (x_format != DQ_ROWS_BF16 && x_format != DQ_ROWS_E4M3 && x_format != DQ_ROWS_E4M3_GROUP64) return DQ_ERR_INVALID_ARG;
@@ -916,9 +917,11 @@ int dq_rows_forward(const void* X, int x_format, long long x_stride, const float
     p.span = (int*)(ws + wl.off_span);
     p.u = (uint16_t*)(ws + wl.off_u);
     p.digits = ws + wl.off_digits;
-    p.budget_ns = kWaitBudgetNs;
+    p.budget_ns = budget_ns;
+    p.u_missing = u_missing;
     cudaError_t e = dq::rows_plan(p);
     if (e != cudaSuccess) return cuda_fail(e, "few-row product");
+    if (u_missing && !p.own_digits) return DQ_ERR_UNSUPPORTED_SHAPE;
     CUtensorMap tm_w, tm_s, tm_x, tm_l2, tm_u;
     if (!map_2d(&tm_w, p.packed_w + pl.off_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Ci / 2, Co, 128, 128))
         return map_fail("weight codes");
@@ -934,6 +937,21 @@ int dq_rows_forward(const void* X, int x_format, long long x_stride, const float
     }
     e = dq::launch_rows(tm_w, tm_s, tm_x, tm_l2, tm_u, p, (cudaStream_t)stream);
     return e == cudaSuccess ? DQ_OK : cuda_fail(e, "few-row product");
+}
+
+int dq_rows_forward(const void* X, int x_format, long long x_stride, const float* x_scales, int rows, int Ci, int Co,
+                    int rank, const void* packed_W, const void* L1_mma, const void* L2_slab, int epilogue, void* Y,
+                    long long y_stride, void* workspace, size_t workspace_bytes, void* stream) {
+    return rows_forward(X, x_format, x_stride, x_scales, rows, Ci, Co, rank, packed_W, L1_mma, L2_slab, epilogue, Y,
+                        y_stride, workspace, workspace_bytes, stream, kWaitBudgetNs, 0);
+}
+
+int dq_selftest_rows_wait(int budget_us, const void* X, int rows, int Ci, int Co, int rank, const void* packed_W,
+                          const void* L1_mma, const void* L2_slab, void* Y, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+    if (budget_us < 1000 || rows < 1) return DQ_ERR_INVALID_ARG;
+    return rows_forward(X, DQ_ROWS_BF16, 0, nullptr, rows, Ci, Co, rank, packed_W, L1_mma, L2_slab, DQ_EPILOGUE_NONE, Y, 0,
+                        workspace, workspace_bytes, stream, (uint64_t)budget_us * 1000ull, 1);
 }
 
 int dq_read_device_status(const void* workspace, void* stream, int* status, int clear) {

@@ -138,6 +138,7 @@ struct RowsParams {
     float* e;                   // rows: what each row's sum of digits is multiplied by
     int* span;                  // rows x parts: positive sum over a row's parts: it is summed without digits
     uint64_t budget_ns;
+    int u_missing;              // arrivals that the exchange of U waits for in vain (dq_selftest_rows_wait; else 0)
     // the cut of the product (rows_plan)
     int n_rows, n_pad, passes;  // rows of X per pass, their digits' columns
     int splits, group;          // parts of the channels, and tiles, of a cluster

@@ -895,7 +895,7 @@ __global__ void __launch_bounds__(product_threads(kForm != kPrepared), kForm == 
             mbar_init(&bars.empty[s], 1);
         }
         for (int i = 0; i < kOwnTurns; i++) mbar_init(&bars.digits[i], kEpiThreads / 32);
-        mbar_init(&bars.u, (uint32_t)csize);
+        mbar_init(&bars.u, (uint32_t)(csize + p.u_missing));
         mbar_init(&bars.accf, 1);
         mbar_init(&bars.acce, 2 * kEpiThreads / 32);
         bars.abort_flag = 0;
@@ -1084,6 +1084,11 @@ __global__ void __launch_bounds__(product_threads(kForm != kPrepared), kForm == 
                         if (!own) bd = b0d;
                     }
                 }
+                if (!ok) {   // the accumulator is not whole: neither CTA's epilogue takes it when it arrives
+                    *abort_flag = 1;
+                    if (pairs) st_dsmem_f32(mapa_shared(smem_u32(&bars.abort_flag), 1), 1.f);
+                    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                }
                 commit(&bars.accf);
             }
             if (used) mbar_wait(&bars.accf, (used - 1) & 1, abort_flag, nullptr, p.budget_ns, false);   // no MMA runs past this point
@@ -1102,6 +1107,8 @@ __global__ void __launch_bounds__(product_threads(kForm != kPrepared), kForm == 
             bars.S_W = __uint_as_float(h.b.z);
             bars.flags = h.b.w;
             bars.fits = fits;
+            // the call's status word, long before a wait of any CTA can have run out and been recorded there
+            if (own && blockIdx.x + blockIdx.y + blockIdx.z == 0) *p.status = fits ? 0 : kStatusBadWeight;
         }
         __syncwarp();
         bar_arrive(6, 32 + kEpiThreads);
@@ -1170,11 +1177,10 @@ __global__ void __launch_bounds__(product_threads(kForm != kPrepared), kForm == 
             form_wide();
             if (own) bar_sync(5, 512);   // the low-rank term
             if (lane == 0) done = mbar_wait(&bars.accf, 0, abort_flag, p.status, p.budget_ns);
-            done = __shfl_sync(0xffffffffu, done, 0);
+            done = __shfl_sync(0xffffffffu, done && !*abort_flag, 0);   // (also where the low-rank term's wait ran out)
             tc_fence_after();
         }
     }
-    if (own && tid == 96 && blockIdx.x + blockIdx.y + blockIdx.z == 0) *p.status = header_ok(load_header(p), p) ? 0 : kStatusBadWeight;
     // This CTA's part of the rows 4 b to 4 b + 3 for the thread's output channel: the digits' columns with
     // weights 8^-p, times S_W and the row's factor, and U L2 where this CTA has it
     auto parts_of = [&](int b, float (&v)[4]) {
@@ -1223,7 +1229,7 @@ __global__ void __launch_bounds__(product_threads(kForm != kPrepared), kForm == 
             // (a warp whose wait has run out goes on without writing, as the others still meet it at the barrier)
             bool full = true;
             if (lane == 0) full = mbar_wait(&bars.accf, used & 1, abort_flag, p.status, p.budget_ns);
-            done = __shfl_sync(0xffffffffu, full, 0) && done;
+            done = __shfl_sync(0xffffffffu, full && !*abort_flag, 0) && done;
             tc_fence_after();
             float v[kPassRows / 8][4];
 #pragma unroll
@@ -1273,9 +1279,11 @@ __global__ void __launch_bounds__(product_threads(kForm != kPrepared), kForm == 
                 }
             }
         }
+        // without this CTA's part no CTA of the tile writes its rows
+        if (epi && !done && lane < splits) st_dsmem_f32(mapa_shared(smem_u32(&bars.abort_flag), (uint32_t)(tile0 + lane)), 1.f);
         __syncwarp();
         cluster_sync();
-        if (epi && done && ok) {
+        if (epi && done && ok && !*abort_flag) {
             for (int n = 2 * group; n < mine; n += 4) {
                 float v0 = 0.f, v1 = 0.f;
                 for (int q = 0; q < splits; q++) {
