@@ -58,6 +58,7 @@
 // (a 16-column exponent slot per stage next to one accumulator).
 #include <atomic>
 
+#include "../../include/deltaquant.h"
 #include "dq_common.h"
 #include "dq_internal.h"
 #include "dq_ptx.cuh"
@@ -218,6 +219,8 @@ __global__ void __launch_bounds__(g_threads(kKind), 1)
     const int m_lo = p.tile_m0, num_m = p.tile_m1 - p.tile_m0;   // this launch's row tiles
     const int num_tiles = num_m * num_n;
     const int nk = p.k_stages, ntot = p.k_stages + p.slab_stages;
+    // the packed weight's header (magic, version, Co, Ci), on its way beside the setup
+    const uint4 head = *reinterpret_cast<const uint4*>(p.packed_w);
 
     if (tid == 0) {
         for (int s = 0; s < S; s++) {
@@ -242,6 +245,16 @@ __global__ void __launch_bounds__(g_threads(kKind), 1)
     cluster_sync();   // barriers of both CTAs initialised, tensor memory allocated
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (head.x != DQ_PACK_MAGIC || head.y != DQ_PACK_FORMAT_VERSION || (int)head.z != p.Nout || (int)head.w != p.Ci) {
+        // a weight of other sizes may end before the sections that this call's sizes point to: nothing of it is read
+        if (blockIdx.x == 0 && tid == 0) atomicCAS(p.status, 0, kStatusBadWeight);
+        cluster_sync();
+        if (warp == 1) {
+            tc_fence_after();
+            tmem_dealloc_pair(tmem, 512);
+        }
+        return;
+    }
     if (kFp8) {
         // the A operand (q8) carries its scale in the epilogue: its MMA scales are 1 (UE8M0 127),
         // written once into four columns of every lane of both CTAs' tensor memory
