@@ -167,3 +167,15 @@ def test_two_branches_of_one_capture(dq, rows):
         torch.cuda.synchronize()
         assert all(torch.equal(t, u) for t, u in zip((n, a, b, z), want))
     del graph
+
+
+@pytest.mark.parametrize("fmt", [0, 1, 2])
+def test_norm_with_the_largest_eps(dq, fmt):
+    x = torch.ldexp(torch.randn(3, 320, generator=torch.Generator().manual_seed(1)), torch.tensor(62)).bfloat16()
+    y = torch.empty(3, 320, dtype=torch.bfloat16 if fmt == 0 else torch.float8_e4m3fn, device="cuda")
+    sc = torch.empty(3, 1 if fmt == 1 else 5, device="cuda") if fmt else None
+    eps = float(torch.finfo(torch.float32).max)
+    dq.dq_rmsnorm_forward(x.cuda(), 3, 320, y, eps=eps, y_format=fmt, y_scales=sc)
+    torch.cuda.synchronize()
+    h, ref = norm_reference(x, None, None, eps)
+    check_norm(dq, h, ref, 320, fmt, None, y.cpu(), sc.cpu() if fmt else None)

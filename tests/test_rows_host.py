@@ -86,3 +86,8 @@ def test_rows_wait_selftest_refusals():
     call = lambda us=50000, m=4: dq._lib.dq_selftest_rows_wait(us, P, m, 512, 256, 32, P, P, P, P, P, 16, None)  # noqa: E731
     assert call(us=999) == dq.DQ_ERR_INVALID_ARG and call(m=0) == dq.DQ_ERR_INVALID_ARG
     assert call() == dq.DQ_ERR_WORKSPACE_TOO_SMALL
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 3.3e38])
+def test_norm_takes_every_finite_eps(eps):
+    assert norm(rows=0, eps=eps) == dq.DQ_OK

@@ -4,6 +4,7 @@
 //   (b) main FP4 product with low-rank slab and scatter epilogue.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <stdio.h>
 #include <string.h>
@@ -825,7 +826,7 @@ int dq_linear_forward_host_ex(const void* X_host, int T, int H, int W, int t, in
 int dq_rmsnorm_forward(const void* X, long long x_stride, const void* residual, long long residual_stride,
                        const void* gamma, long long rows, int C, float eps, void* sum_out, long long sum_stride,
                        int y_format, void* Y, long long y_stride, float* y_scales, void* stream) {
-    if (rows < 0 || C < 1 || !(eps >= 0.f) || eps > 3.0e38f) return DQ_ERR_INVALID_ARG;
+    if (rows < 0 || C < 1 || !(eps >= 0.f) || isinf(eps)) return DQ_ERR_INVALID_ARG;
     if (y_format != DQ_ROWS_BF16 && y_format != DQ_ROWS_E4M3 && y_format != DQ_ROWS_E4M3_GROUP64) return DQ_ERR_INVALID_ARG;
     if (rows >= (1ll << 31) || C > 32768) return DQ_ERR_UNSUPPORTED_SHAPE;
     const bool codes = y_format != DQ_ROWS_BF16;
