@@ -56,7 +56,7 @@ def reference(w, v, fmt):
     lossy = (v != 0) & (v.abs() < T)
     part = lossy.sum(1) / (v != 0).sum(1)
     assert ((part < 0.09) | (part > 0.2)).all()   # clearly on one side, in each part of the channels too
-    off = 2.0 ** -23 * M * (lossy if fmt == 0 else v != 0) * (part <= 0.125)[:, None]
+    off = 2.0 ** -23 * M * (lossy if fmt == 0 else (v != 0) & (fmt == 2)) * (part <= 0.125)[:, None]
     tol = off @ w_t(wv.abs()) + 2 * U * (w.Ci / 16 + 32) * A + (2 * U * (w.Ci / 16 + 2 * w.rank + 32) + 2.0 ** -16) * B
     return y, tol + 2.0 ** -8 * y.abs() + 2.0 ** -133
 

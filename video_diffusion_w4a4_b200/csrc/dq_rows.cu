@@ -33,9 +33,10 @@
 //                    L1, which the product multiplies with L2 as BF16 K steps (hi +
 //                    lo) into columns of their own.
 //
-// Up to kOwnRows rows k_rows_product does all of it (one launch): the warps that
-// write the output write the digits of the CTA's channels before it, and eight more
-// form the low-rank term beside the product.  The CTAs of a cluster, parts of tiles
+// With few rows k_rows_product does all of it (one launch): up to four where a CTA's
+// digits and a ring of six stages fit, five to kOwnRows where it has four stages at most
+// (rows_plan, own_turns).  The warps that write the output write the digits of the CTA's
+// channels before it, and eight more form the low-rank term beside the product.  The CTAs of a cluster, parts of tiles
 // and whole ones, take a share of the channels of U each and exchange their sums
 // through distributed shared memory, so that L1 is read once a cluster.
 //
@@ -44,9 +45,9 @@
 // channels (2 with pairs).  Measured on B200, calls one after another on weights that
 // are not in L2, against the time that the bytes of weight, factors, X and Y need at
 // the HBM's copy rate:
-//   1 x 5120 -> 5120     9.4 us (2.4)      1 x 5120 -> 13824   13.7 us (6.3)
-//   4 x 13824 -> 5120   15.9 us (6.3)     21 x 5120 -> 13824   16.0 us (6.4)
-//   77 x 2048 -> 5120   12.2 us (1.3)    512 x 5120 -> 5120    57 us (4.0; 16 at the
+//   1 x 5120 -> 5120     9.0 us (2.4)      1 x 5120 -> 13824   14.2 us (6.3)
+//   4 x 13824 -> 5120   14.4 us (6.3)     21 x 5120 -> 13824   16.5 us (6.4)
+//   77 x 2048 -> 5120   12.7 us (1.3)    512 x 5120 -> 5120    60 us (4.0; 16 at the
 //   BF16 tensor rate)
 // The stream alone, the same copies without any MMAs, takes 3.3 us for 5120 -> 5120
 // and 7.1 us for 5120 -> 13824 (5.6 TB/s); a launch that waits for the one before it
@@ -63,8 +64,8 @@
 // Once the weight streams, a load of anything else waits behind it for 2 to 4 us, a
 // ring of the weight's stages per SM deep.  So the other loads come first, or where
 // nothing waits for them: k_rows_product holds the stream back until they are under
-// way (5120 -> 5120: 9.4 us against 9.8 us without; 5120 -> 13824: 13.7 against 13.1,
-// 13824 -> 5120 with 4 rows the same either way), and k_rows_prepare lets the product
+// way (before the header's check: 5120 -> 5120 9.4 us against 9.8 us without, 5120 -> 13824
+// 13.7 against 13.1, 13824 -> 5120 with 4 rows the same either way), and k_rows_prepare lets the product
 // in when its own have arrived (programmatic launch).
 #include "../../include/deltaquant.h"
 #include "dq_common.h"
@@ -81,9 +82,12 @@ constexpr int kDigits = 8;                       // FP4 digits of a value
 constexpr int kPassRows = 32;                    // rows of X per CTA: 256 MMA columns
 constexpr int kOwnRows = 8;                      // up to so many rows the product writes the digits itself
 constexpr int kOwnTurns = 10;                    // pieces of eight channels a thread holds for that at most
-// ... and uses: with a warp to a row seven of them take longer than k_rows_prepare (8 rows, 5120 -> 5120: 12.2 us
-// against 11.2 us), one does not (1536 -> 1536: 8.1 us against 8.9 us); with two warps or more to a row ten do not
-// either (4 rows, 5120 -> 13824: 14.2 us against 14.7 us; 13824 -> 5120: 16.0 us against 18.4 us).
+// ... and uses: with a warp to a row (five rows and more) six and seven of them take longer than k_rows_prepare (8 rows:
+// 4608 -> 5120 10.9 us against 10.5, 5120 -> 5120 11.5 against 10.5), four and fewer do not (2560 -> 5120 9.9 us against
+// 10.1, 2048 -> 5120 9.3 against 10.7, 1280 -> 5120 9.0 against 10.8, 1536 -> 1536 7.8 against 10.1); five are as good
+// either way (3840 -> 5120 10.2 against 10.7).  With two warps or more to a row ten take less (when measured, 4 rows,
+// 5120 -> 13824: 14.2 us against 14.7 us; 13824 -> 5120: 16.0 us against 18.4 us).  A thread holds all of them in
+// registers, whatever the row count: the E4M3 forms spill some 90 bytes of their 96 registers for it.
 constexpr int own_turns(int rows) { return rows <= 4 ? kOwnTurns : 4; }
 // producers of A and B, MMA, a spare warp, eight epilogue warps; eight for the low-rank term
 constexpr int product_threads(bool own) { return own ? 640 : 384; }
@@ -1390,8 +1394,9 @@ cudaError_t prepare_plan(RowsParams& p) {
     if (e != cudaSuccess) return e;
     // A CTA per row's piece and clusters of eight, while they are no more than four times what fits at once (64
     // registers a thread); else as many CTAs as fit, half of them low-rank ones at most, in smaller clusters, and
-    // the others take piece after piece.  5120 -> 5120: 256 rows 42.1 us either way, 512 rows 71 us against 62 us;
-    // 256 rows 5120 -> 13824: 76.5 us against 79 us.
+    // the others take piece after piece.  One CTA a piece against this: 5120 -> 5120 256 rows 39.8 us either way, 512 rows
+    // 67 us against 58.5, 1024 rows 121 against 102; 256 rows 13824 -> 5120 85 us against 88, 512 rows 146 against 132;
+    // 1024 rows 2048 -> 5120 59 us either way.  384 rows 5120 -> 5120, just below the bound, would take 46 us for 53.
     const long long fit = (long long)sms * (1024 / prep_threads(p.Ci)), groups = cdiv(p.rows, 16) * cdiv(p.rank, 32);
     long long pieces = (long long)p.rows * rows_parts(p.Ci);
     p.prep_cluster = kPrepCluster;
